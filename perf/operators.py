@@ -199,8 +199,6 @@ def prepare(case, seed):
         elif op == "matvec":
             st["w"] = layer.W4Weight(*t["w"], group=case["group"])
             st["y"] = torch.empty((case["S"], case["N"]), dtype=torch.bfloat16, device=DEV)
-            st["ws"] = torch.empty(moe.moe_w4_matvec_workspace_bytes(
-                case["S"], case["K"], case["N"]), dtype=torch.uint8, device=DEV)
         else:
             pack = lambda n: layer.W4Weight(*t[n], group=case["group"]) if n in t else None
             st["buf"] = layer.W4MoEBuffers(case["S"], case["H"], case["D"], case["E"], case["k"],
@@ -228,7 +226,7 @@ def _run_own(st):
     if op == "ffn_bwd":
         return st["buf"].backward(t["do"], t["x"], t["wu"], t["wg"], t["wd"], t["u"], t["g"])
     if op == "matvec":
-        moe.moe_w4_matvec(t["x"], st["w"], st["y"], workspace=st["ws"])
+        moe.moe_w4_matvec(t["x"], st["w"], st["y"])
         return st["y"]
     return st["buf"].forward(t["x"], *st["wt"], topk_ids=t["ids"], topk_weights=t["w"])
 
