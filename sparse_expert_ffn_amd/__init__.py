@@ -141,6 +141,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                  "moe_profile_collect", "moe_device_query", "moe_trace_attach"):
         getattr(lib, name).restype = ctypes.c_int
     del i64
+    from . import ffn
+    ffn.bind(lib)
     if path is None:
         _LIB = lib
     return lib
@@ -327,3 +329,10 @@ def moe_trace_attach(buffer, check=True) -> int:
     if check:
         _check("moe_trace_attach", code)
     return code
+
+
+# layer norm, the dense feed-forward block, 4-bit weights (include/moe_ffn.h)
+from .ffn import *  # noqa: E402,F401,F403
+from .ffn import FFN_EXPORTS, __all__ as _ffn_all  # noqa: E402
+
+__all__ += [*_ffn_all, "FFN_EXPORTS"]

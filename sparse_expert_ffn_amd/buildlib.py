@@ -24,7 +24,8 @@ HIPCC_FLAGS = [
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(PKG, "csrc", "*.hip")))
+    return sorted(glob.glob(os.path.join(PKG, "csrc", "*.hip")) +
+                  glob.glob(os.path.join(PKG, "csrc", "ffn", "*.hip")))
 
 
 def _code_only(text: str) -> str:
@@ -39,14 +40,15 @@ def _code_only(text: str) -> str:
 
 def source_digest() -> str:
     """SHA-256 over what determines the compiled kernels: the code of the HIP
-    sources and headers under csrc/ and of the public header (comments and
+    layer's sources and headers in csrc/ and of its public header (comments and
     layout left out, so a comment edit keeps the digest) and the compiler
-    flags. Measurement records (hardware counters) carry it, so that a record
+    flags. The operators in csrc/ffn/ (public header moe_ffn.h) are compiled
+    apart from them and do not count. Measurement records (hardware counters) carry it, so that a record
     taken on other kernels is recognised as stale."""
     import hashlib
     h = hashlib.sha256()
-    files = sorted(glob.glob(os.path.join(PKG, "csrc", "*"))) + \
-        sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
+    files = sorted(f for f in glob.glob(os.path.join(PKG, "csrc", "*")) if os.path.isfile(f)) + \
+        [os.path.join(ROOT, "include", "moe.h")]
     for f in files:
         h.update(os.path.relpath(f, ROOT).encode())
         with open(f, encoding="utf-8") as fh:
@@ -71,7 +73,8 @@ def build(verbose: bool = False, extra: list[str] | None = None, out: str = LIB)
     """Each source compiled to an object side by side, then one link."""
     from concurrent.futures import ThreadPoolExecutor
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    inc = ["-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc")]
+    inc = ["-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
+           "-I", os.path.join(PKG, "csrc", "ffn")]
     flags = [f for f in HIPCC_FLAGS if f != "-shared"]
     objdir = os.path.join(ROOT, "_build", os.path.basename(out))
     os.makedirs(objdir, exist_ok=True)

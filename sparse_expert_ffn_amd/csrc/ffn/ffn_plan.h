@@ -1,0 +1,187 @@
+// Which tile and how many splits of K a product of the feed-forward block takes,
+// and its launch.
+#pragma once
+
+#include "ffn_gemm.h"
+
+namespace moe {
+
+// A tile: rows x columns (of all panels), and what the choice goes by (from
+// measurement, in ns): one K stage of a workgroup that has a CU to itself, and
+// what a workgroup costs beyond its stages (first loads, epilogue).
+struct TileCost {
+  int bm, bn;
+  int bk;
+  float stage_ns, fixed_ns;
+};
+constexpr TileCost kBfTiles[] = {
+    {256, 256, 64, 1100.f, 3000.f},
+    {128, 128, 64, 400.f, 2500.f},
+    {64, 128, 64, 260.f, 2500.f},
+    {16, 128, 64, 200.f, 2500.f},
+};
+constexpr TileCost kF32Tiles[] = {
+    {128, 128, 16, 1000.f, 2500.f},
+    {64, 64, 16, 300.f, 2000.f},
+};
+constexpr int kCus = 256;
+
+struct GemmPlan {
+  int tile;          // index into the table
+  int stages, split_stages, splits;
+  int tiles_m, tiles_n;
+  size_t part_bytes;
+};
+
+// The tile and the splits with the least estimated time: rounds of workgroups
+// over the CUs times a workgroup's time, plus the splits' sums' way through memory.
+// `tiles`: bit mask of the tiles that the product has kernels for.
+inline GemmPlan plan_gemm(bool f32, unsigned tiles, bool dual, int64_t M, int64_t N, int64_t K,
+                          int pairs) {
+  GemmPlan best = {};
+  float best_ns = 3.0e38f;
+  const int n = f32 ? 2 : 4;
+  for (int t = 0; t < n; ++t) {
+    if (!(tiles >> t & 1)) continue;
+    const TileCost& c = f32 ? kF32Tiles[t] : kBfTiles[t];
+    GemmPlan p = {};
+    p.tile = t;
+    p.stages = (int)((K + c.bk - 1) / c.bk) * pairs;
+    p.tiles_m = (int)((M + c.bm - 1) / c.bm);
+    const int cols = dual ? c.bn / 2 : c.bn;
+    p.tiles_n = (int)((N + cols - 1) / cols);
+    const int64_t wgs = (int64_t)p.tiles_m * p.tiles_n;
+    for (int s = 1; s <= 32 && s <= p.stages; ++s) {
+      p.split_stages = (p.stages + s - 1) / s;
+      p.splits = (p.stages + p.split_stages - 1) / p.split_stages;
+      if (p.splits != s) continue;
+      if (s > 1 && wgs * s > 4 * kCus) break;
+      const float rounds = (float)((wgs * s + kCus - 1) / kCus);
+      float ns = rounds * (c.fixed_ns + p.split_stages * c.stage_ns);
+      p.part_bytes = 0;
+      if (s > 1) {
+        p.part_bytes = (size_t)s * (dual ? 2 : 1) * (size_t)M * (size_t)N * 4;
+        ns += 3000.f + (float)p.part_bytes * 2.f / 4000.f;
+      }
+      if (ns < best_ns) {
+        best_ns = ns;
+        best = p;
+      }
+    }
+  }
+  return best;
+}
+
+inline void apply_plan(const GemmPlan& p, GemmArgs* g, void* part) {
+  g->stages = p.stages;
+  g->split_stages = p.split_stages;
+  g->splits = p.splits;
+  g->tiles_m = p.tiles_m;
+  g->tiles_n = p.tiles_n;
+  g->part = (float*)part;
+}
+
+template <typename Core, typename EP>
+void launch_tile(const GemmArgs& g, const EP& ep, hipStream_t st) {
+  const unsigned grid = (unsigned)((int64_t)g.tiles_m * g.tiles_n * g.splits);
+  gemm_kernel<Core, EP><<<grid, Core::THREADS, 0, st>>>(g, ep);
+  if (g.splits > 1) {
+    const int64_t n = g.M * ((g.N + 3) / 4);
+    const int64_t b = (n + 255) / 256;
+    gemm_join_kernel<Core::DUAL, EP><<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(g, ep);
+  }
+}
+
+// The tiles of a product with these operand orders.
+template <bool DUAL, bool AKC, bool BKC>
+constexpr unsigned tile_mask(bool f32) {
+  return f32 ? 3u : AKC ? 15u : 7u;  // 16 rows: K-contiguous A only
+}
+
+template <typename T, bool DUAL, bool AKC, bool BKC, typename EP>
+void launch_gemm(const GemmPlan& p, const GemmArgs& g, const EP& ep, hipStream_t st) {
+  if constexpr (sizeof(T) == 4) {
+    if (p.tile == 0)
+      launch_tile<F32Core<128, 128, 2, DUAL, AKC, BKC>>(g, ep, st);
+    else
+      launch_tile<F32Core<64, 64, 2, DUAL, AKC, BKC>>(g, ep, st);
+  } else {
+    constexpr int NP = DUAL ? 2 : 1;
+    if (p.tile == 0)
+      launch_tile<BfCore<256, 256, 2, DUAL, AKC, BKC, 2, 4, 2>>(g, ep, st);
+    else if (p.tile == 1)
+      launch_tile<BfCore<128, 128, NP, DUAL, AKC, BKC, 2, 4, 4>>(g, ep, st);
+    else if (p.tile == 2)
+      launch_tile<BfCore<64, 128, NP, DUAL, AKC, BKC, 2, 4, 6>>(g, ep, st);
+    else if constexpr (AKC)
+      launch_tile<BfCore<16, 128, NP, DUAL, AKC, BKC, 1, 4, 8>>(g, ep, st);
+  }
+}
+
+// ------------------------------------------------------------ epilogues
+// h = SiLU(u) g from the fp32 sums; u and g kept for a backward pass.
+template <typename T>
+struct EpSwiglu {
+  T *h, *U, *G;
+  int64_t ld;
+  __device__ __forceinline__ void operator()(int64_t m, int64_t n, f32x4_t u, f32x4_t g) const {
+    const int64_t o = m * ld + n;
+    f32x4_t v;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = silu_f32(u[r]) * g[r];
+    store4(h + o, v);
+    if (U != nullptr) {
+      store4(U + o, u);
+      store4(G + o, g);
+    }
+  }
+};
+template <typename T>
+struct EpStore {
+  T* out;
+  int64_t ld;
+  __device__ __forceinline__ void operator()(int64_t m, int64_t n, f32x4_t v, f32x4_t) const {
+    store4(out + m * ld + n, v);
+  }
+};
+template <typename T>
+struct EpStore2 {
+  T *out0, *out1;
+  int64_t ld;
+  __device__ __forceinline__ void operator()(int64_t m, int64_t n, f32x4_t v0, f32x4_t v1) const {
+    store4(out0 + m * ld + n, v0);
+    store4(out1 + m * ld + n, v1);
+  }
+};
+// From dh: dU, dG, and h again (all operands of the products that follow); h may
+// be null (frozen weights).
+template <typename T>
+struct EpSwigluBwd {
+  const T *U, *G;
+  T *dU, *dG, *h;
+  int64_t ld;
+  __device__ __forceinline__ void operator()(int64_t m, int64_t n, f32x4_t dh, f32x4_t) const {
+    const int64_t o = m * ld + n;
+    const f32x4_t u = load4(U + o), g = load4(G + o);
+    f32x4_t du, dg, hv;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-u[r]));
+      const float a = u[r] * s;
+      dg[r] = dh[r] * a;
+      du[r] = dh[r] * g[r] * (s * (1.0f + u[r] * (1.0f - s)));
+      hv[r] = a * g[r];
+    }
+    store4(dU + o, du);
+    store4(dG + o, dg);
+    if (h != nullptr) store4(h + o, hv);
+  }
+};
+
+// Clears n floats' worth of bytes (a kernel: a captured graph holds no memset).
+hipError_t launch_zero(void* p, size_t bytes, hipStream_t st);
+
+// What both passes' entry points check first.
+moe_status check_ffn(const moe_ffn_shape* s);
+
+}  // namespace moe

@@ -1,0 +1,576 @@
+// Products with 4-bit weights for decode (include/moe_ffn.h).
+//
+// Decode is bound by the weights' bytes: a weight is read once and meets at most
+// 16 rows. One MFMA (16x16x32, bf16) takes 16 rows, so one row or sixteen cost
+// the same and the matrix cores idle next to HBM either way; what matters is
+// that the codes stream and that unpacking them stays cheap.
+//
+// Unpacking: a bf16 with the exponent of 16 has steps of 1/8, so its bits
+// 3..6 hold a code exactly: 0x4180 | code << 3 = 16 + code. The packed dword
+// (8 codes, rotated left by 3) gives two such values with one rotation and one
+// and-or per pair. The MFMA sums X (16 + code); what is too much, 24 X, is
+// summed by MFMAs with a constant -24 operand into the accumulator that the
+// group's product starts from (once for all columns and matrices of a wave),
+// which leaves sum X (code - 8). Products are exact in fp32 (8 x 8 bits), and
+// the group's sum is scaled in fp32 by the column's scale, so W is never rounded.
+// (0x4300 | code = 128 + code would save a rotation and lose 3 more bits.)
+//
+// Layout: tiles of 16 columns x 128 rows, 1 KB of codes in the order of the
+// MFMA operand (lane l: column l % 16, rows 8 (l / 16) .. + 7 of each 32) and
+// the scales behind them: a wave streams a column tile as contiguous memory,
+// 16 bytes per lane and load.
+#include "ffn_common.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTileK = 128, kTileN = 16;
+constexpr int64_t kMaxDim = 1 << 22;
+constexpr int64_t kMaxRows = 4096;
+constexpr int64_t kMaxExperts = 1 << 16;
+constexpr int64_t kMaxTiles = 1 << 25;  // waves of a launch, below 2^32 threads
+
+__host__ __device__ constexpr int tile_bytes(int group) { return 1024 + kTileK / group * 32; }
+__host__ __device__ inline int64_t tiles_k(int64_t K) { return (K + kTileK - 1) / kTileK; }
+__host__ __device__ inline int64_t tiles_n(int64_t N) { return (N + kTileN - 1) / kTileN; }
+
+bool group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
+
+template <typename T>
+__global__ void w4_quantize_kernel(const T* W, int64_t E, int64_t K, int64_t N, int group,
+                                   uint8_t* codes, bf16_t* scales) {
+  const int64_t ng = (K + group - 1) / group;
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= E * ng * N) return;
+  const int64_t n = i % N, g = i / N % ng, e = i / N / ng;
+  const int64_t k0 = g * group, k1 = k0 + group < K ? k0 + group : K;
+  const T* w = W + e * K * N + n;
+  float top = 0.f;
+  for (int64_t k = k0; k < k1; ++k) top = fmaxf(top, fabsf(to_f32<T>(w[k * N])));
+  const bf16_t sb = f32_to_bf16(top / 7.0f);
+  const float s = bf16_to_f32(sb);
+  scales[(e * ng + g) * N + n] = sb;
+  for (int64_t k = k0; k < k1; ++k) {
+    // s = 0 (a group of zeros, or too small for a bf16 scale): code 8
+    const float q = s > 0.f ? rintf(to_f32<T>(w[k * N]) / s) : 0.f;
+    codes[(e * K + k) * N + n] = (uint8_t)(int)(fminf(fmaxf(q, -8.f), 7.f) + 8.f);
+  }
+}
+
+__global__ void w4_pack_kernel(const uint8_t* codes, const bf16_t* scales, int64_t E, int64_t K,
+                               int64_t N, int group, char* packed) {
+  const int64_t nt = tiles_n(N), kt = tiles_k(K), ng = (K + group - 1) / group;
+  const int64_t tile = (int64_t)blockIdx.x * (blockDim.x / 64) + threadIdx.x / 64;
+  if (tile >= E * nt * kt) return;
+  const int64_t e = tile / (nt * kt), ct = tile / kt % nt, kk = tile % kt;
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+  const int64_t n = ct * kTileN + c;
+  char* out = packed + tile * tile_bytes(group);
+  uint32_t w[4];
+  for (int i = 0; i < 4; ++i) {
+    uint32_t v = 0;
+    for (int j = 0; j < 8; ++j) {
+      const int64_t k = kk * kTileK + 32 * i + 8 * q + j;
+      const uint32_t code = k < K && n < N ? codes[(e * K + k) * N + n] & 15u : 8u;
+      v |= code << (4 * (j / 2) + 16 * (j % 2));
+    }
+    w[i] = (v << 3) | (v >> 29);
+  }
+  *reinterpret_cast<uint4*>(out + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = lane; i < kTileK / group * kTileN; i += 64) {
+    const int64_t g = kk * (kTileK / group) + i / kTileN, m = ct * kTileN + i % kTileN;
+    reinterpret_cast<bf16_t*>(out + 1024)[i] =
+        g < ng && m < N ? scales[(e * ng + g) * N + m] : (bf16_t)0;
+  }
+}
+
+__device__ __forceinline__ f32x4_t mfma(uint4 a, uint4 b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                 __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// 8 codes of a packed dword as bf16 values 16 + code, rows ascending.
+__device__ __forceinline__ uint4 unpack(uint32_t w) {
+  constexpr uint32_t m = 0x00780078u, o = 0x41804180u;
+  return make_uint4((w & m) | o, ((w >> 4) & m) | o, ((w >> 8) & m) | o,
+                    (__builtin_amdgcn_alignbit(w, w, 12) & m) | o);
+}
+
+// What a wave holds of one 128-row step: its column tiles' codes and scales and
+// 16 rows of X.
+template <int G, int NP>
+struct Step {
+  static constexpr int NG = kTileK / G;
+  uint4 a[4];
+  uint4 c[NP];
+  bf16_t s[NP][NG];
+
+  // x: this lane's row of X at k = 8 (lane / 16), or null (row of zeros);
+  // w: the column tiles; kleft: values of K from this step on, less 8 (lane / 16)
+  __device__ __forceinline__ void load(const bf16_t* x, const char* const (&w)[NP], int kt,
+                                       int64_t kleft) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const char* t = w[p] + (int64_t)kt * tile_bytes(G);
+      c[p] = *reinterpret_cast<const uint4*>(t + lane * 16);
+      const bf16_t* sp = reinterpret_cast<const bf16_t*>(t + 1024) + (lane & 15);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) s[p][g] = sp[g * kTileN];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a[i] = x != nullptr && 32 * i < kleft
+                 ? *reinterpret_cast<const uint4*>(x + (int64_t)kt * kTileK + 32 * i)
+                 : make_uint4(0, 0, 0, 0);
+  }
+
+  __device__ __forceinline__ void compute(f32x4_t (&acc)[NP]) const {
+    constexpr uint32_t m24 = 0xC1C0C1C0u;  // -24, -24
+    const uint4 bias = make_uint4(m24, m24, m24, m24);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      f32x4_t start = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < G / 32; ++i) start = mfma(a[g * (G / 32) + i], bias, start);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        f32x4_t t = start;
+#pragma unroll
+        for (int i = 0; i < G / 32; ++i) {
+          const int k = g * (G / 32) + i;
+          const uint32_t w = k == 0 ? c[p].x : k == 1 ? c[p].y : k == 2 ? c[p].z : c[p].w;
+          t = mfma(a[k], unpack(w), t);
+        }
+        const float sc = bf16_to_f32(s[p][g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[p][r] += sc * t[r];
+      }
+    }
+  }
+};
+
+// One wave's share of the product of up to 16 rows with NP column tiles: every
+// wk-th 128-row step from step w0 on. Lane l ends with column l % 16 of rows
+// 4 (l / 16) .. + 3.
+template <int G, int NP>
+__device__ __forceinline__ void wave_product(const bf16_t* row, const char* const (&w)[NP],
+                                             int64_t K, int w0, int wk, f32x4_t (&acc)[NP]) {
+  const int kt_n = (int)tiles_k(K);
+  const int q8 = ((threadIdx.x & 63) >> 4) * 8;
+  const bf16_t* x = row == nullptr ? nullptr : row + q8;
+  auto left = [&](int kt) { return K - q8 - (int64_t)kt * kTileK; };
+#pragma unroll
+  for (int p = 0; p < NP; ++p) acc[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  Step<G, NP> s0, s1;
+  int kt = w0;
+  if (kt < kt_n) s0.load(x, w, kt, left(kt));
+  while (kt < kt_n) {
+    if (kt + wk < kt_n) s1.load(x, w, kt + wk, left(kt + wk));
+    s0.compute(acc);
+    kt += wk;
+    if (kt >= kt_n) break;
+    if (kt + wk < kt_n) s0.load(x, w, kt + wk, left(kt + wk));
+    s1.compute(acc);
+    kt += wk;
+  }
+}
+
+// The rows of the workgroup's list (f indexes) that blockIdx's entry stands for:
+//   by_row: entry y stands for ids[y]'s expert if no earlier row has it;
+//   else:   entry y stands for expert y.
+// Fills list (LDS) with the rows whose id is that expert, in no particular
+// order (rows do not meet in the products), and returns their number.
+__device__ __forceinline__ int collect_rows(const int32_t* ids, int F, int E, bool by_row, int y,
+                                            int* list, int* count, int* expert) {
+  const int e = by_row ? ids[y] : y;
+  *expert = e;
+  if (e < 0 || e >= E) return 0;  // the same for every thread
+  if (threadIdx.x == 0) count[0] = count[1] = 0;
+  __syncthreads();
+  for (int f = threadIdx.x; f < F; f += blockDim.x)
+    if (ids[f] == e) {
+      if (by_row && f < y) count[1] = 1;
+      list[atomicAdd(&count[0], 1)] = f;
+    }
+  __syncthreads();
+  return count[1] ? 0 : count[0];
+}
+
+struct W4Args {
+  const bf16_t* X;        // rows of K values
+  const char* w[2];       // packed matrices (up and gate, or one)
+  const char* ws[2];      // the shared expert's
+  const int32_t* ids;     // [F] or null: every row takes matrix 0
+  void* out;              // upgate: h [F][N]; matvec: Y [F][N]; down: slots [F][N] fp32
+  void* outs;             // the shared expert's rows
+  const bf16_t* Xs;       // the shared expert's input rows
+  int64_t K, N;           // routed: K values per row, N columns
+  int64_t Ks, Ns;         // shared
+  int F, E, k, S;         // routed rows, matrices, routed rows per row of X, shared rows
+  int by_row, entries;    // collect_rows' entries in use
+  int groups, groups_s;   // workgroups per entry (routed, shared)
+  int wk;                 // waves that share a column tile's K
+  int out_f32;
+};
+
+enum { kMatvec, kUpgate, kDown };
+
+// Workgroup b: column tiles of one entry. Its waves are wn column tiles by wk
+// shares of K; the shares are added in wave order through LDS.
+template <int G, int OP>
+__global__ __launch_bounds__(1024) void w4_kernel(W4Args p) {
+  constexpr int NP = OP == kUpgate ? 2 : 1;
+  extern __shared__ char smem[];
+  __shared__ int count[2];
+  const int waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  float* red = reinterpret_cast<float*>(smem);                     // [waves][NP][256]
+  int* list = reinterpret_cast<int*>(smem + waves * NP * 1024);    // [F]
+  const int wk = p.wk, wn = waves / wk;
+
+  int64_t b = blockIdx.x;
+  const int64_t routed = (int64_t)p.entries * p.groups;
+  const bool shared = b >= routed;
+  int n_rows, e = 0, row0 = 0, y, grp;
+  if (shared) {
+    b -= routed;
+    y = (int)(b / p.groups_s);
+    grp = (int)(b % p.groups_s);
+    row0 = 16 * y;
+    n_rows = p.S - row0 < 16 ? p.S - row0 : 16;
+  } else {
+    y = (int)(b / p.groups);
+    grp = (int)(b % p.groups);
+    if (p.ids == nullptr) {
+      row0 = 16 * y;
+      n_rows = p.F - row0 < 16 ? p.F - row0 : 16;
+    } else {
+      n_rows = collect_rows(p.ids, p.F, p.E, p.by_row, y, list, count, &e);
+    }
+  }
+  const bool listed = !shared && p.ids != nullptr;
+  const int64_t K = shared ? p.Ks : p.K, N = shared ? p.Ns : p.N;
+  const int64_t ct = (int64_t)grp * wn + wave / wk;
+  const bool has_tile = ct < tiles_n(N);
+  if (OP == kMatvec && listed) {
+    // rows without an expert: zeros, written by the row's own entry, or by the
+    // entry behind the experts
+    if (p.by_row ? (e < 0 || e >= p.E) : y == p.E) {
+      for (int f = p.by_row ? y : 0; f < (p.by_row ? y + 1 : p.F); ++f) {
+        const int id = p.ids[f];
+        if (id >= 0 && id < p.E) continue;
+        for (int64_t c = (int64_t)grp * wn * kTileN + threadIdx.x;
+             c < N && c < (int64_t)(grp + 1) * wn * kTileN; c += blockDim.x) {
+          if (p.out_f32)
+            reinterpret_cast<float*>(p.out)[f * N + c] = 0.f;
+          else
+            reinterpret_cast<bf16_t*>(p.out)[f * N + c] = 0;
+        }
+      }
+      return;
+    }
+  }
+  if (n_rows == 0) return;
+
+  const char* w[NP];
+#pragma unroll
+  for (int m = 0; m < NP; ++m)
+    w[m] = (shared ? p.ws[m] : p.w[m]) +
+           ((int64_t)e * tiles_n(N) + (has_tile ? ct : 0)) * tiles_k(K) * tile_bytes(G);
+  const bf16_t* X = shared ? p.Xs : p.X;
+  for (int r0 = 0; r0 < n_rows; r0 += 16) {
+    auto row_of = [&](int r) { return listed ? list[r0 + r] : row0 + r0 + r; };
+    const int lr = lane & 15;
+    const bf16_t* x = nullptr;
+    if (r0 + lr < n_rows) {
+      const int f = row_of(lr);
+      x = X + (int64_t)(listed && OP == kUpgate ? f / p.k : f) * K;
+    }
+    f32x4_t acc[NP];
+    if (has_tile) {
+      wave_product<G, NP>(x, w, K, wave % wk, wk, acc);
+#pragma unroll
+      for (int m = 0; m < NP; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          red[(wave * NP + m) * 256 + (4 * (lane >> 4) + r) * 16 + lr] = acc[m][r];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < wn * 256; i += blockDim.x) {
+      const int t = i >> 8, r = (i >> 4) & 15, c = i & 15;
+      const int64_t n = ((int64_t)grp * wn + t) * kTileN + c;
+      if (r0 + r >= n_rows || n >= N) continue;
+      float v[NP];
+#pragma unroll
+      for (int m = 0; m < NP; ++m) {
+        v[m] = red[(t * wk * NP + m) * 256 + (i & 255)];
+        for (int q = 1; q < wk; ++q) v[m] += red[((t * wk + q) * NP + m) * 256 + (i & 255)];
+      }
+      const int64_t o = (int64_t)row_of(r) * N + n;
+      void* out = shared ? p.outs : p.out;
+      if constexpr (OP == kUpgate)
+        reinterpret_cast<bf16_t*>(out)[o] = f32_to_bf16(silu_f32(v[0]) * v[1]);
+      else if (OP == kDown || p.out_f32)
+        reinterpret_cast<float*>(out)[o] = v[0];
+      else
+        reinterpret_cast<bf16_t*>(out)[o] = f32_to_bf16(v[0]);
+    }
+    if (r0 + 16 < n_rows) __syncthreads();
+  }
+}
+
+// O_t = sum_j w_tj slot_tj (+ the shared row), slots without an expert skipped.
+template <typename T>
+__global__ void w4_combine_kernel(int64_t S, int64_t H, int k, int E, const int32_t* ids,
+                                  const float* w, const float* slots, const float* shared,
+                                  T* O) {
+  const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  if (i >= S * H) return;
+  const int64_t t = i / H, c = i % H;
+  f32x4_t a = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < k; ++j) {
+    const int id = ids[t * k + j];
+    if (id < 0 || id >= E) continue;
+    const float wj = w[t * k + j];
+    const f32x4_t v = load4(slots + (t * k + j) * H + c);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) a[r] += wj * v[r];
+  }
+  if (shared != nullptr) {
+    const f32x4_t v = load4(shared + t * H + c);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) a[r] += v[r];
+  }
+  store4(O + i, a);
+}
+
+moe_status enqueued() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+// Waves that share one column tile's K (wk) and column tiles per workgroup (wn):
+// about 16 waves on each of the 256 CUs in all, as far as K has steps to share.
+void wave_shape(int64_t tiles, int64_t K, int* wk, int* wn) {
+  int s = 1;
+  while (s < 16 && s * 2 <= tiles_k(K) && tiles * s < 4096) s *= 2;
+  *wk = s;
+  *wn = s >= 4 ? 1 : 4 / s;
+}
+
+template <int OP>
+void launch_w4(int group, W4Args& p, int64_t row_blocks, int64_t row_blocks_s, hipStream_t st) {
+  int wn;
+  const int64_t ct = tiles_n(p.N), cts = row_blocks_s ? tiles_n(p.Ns) : 0;
+  wave_shape(row_blocks * ct + row_blocks_s * cts, p.K, &p.wk, &wn);
+  p.entries = (int)row_blocks;
+  p.groups = (int)((ct + wn - 1) / wn);
+  p.groups_s = (int)((cts + wn - 1) / wn);
+  const int waves = p.wk * wn;
+  const size_t lds = (size_t)waves * (OP == kUpgate ? 2048 : 1024) +
+                     (p.ids != nullptr ? (size_t)p.F * sizeof(int) : 0);
+  const unsigned grid = (unsigned)(row_blocks * p.groups + row_blocks_s * p.groups_s);
+  if (group == 32)
+    w4_kernel<32, OP><<<grid, 64 * waves, lds, st>>>(p);
+  else if (group == 64)
+    w4_kernel<64, OP><<<grid, 64 * waves, lds, st>>>(p);
+  else
+    w4_kernel<128, OP><<<grid, 64 * waves, lds, st>>>(p);
+}
+
+moe_status check_w4(int64_t E, int64_t K, int64_t N, int32_t group) {
+  if (E < 1 || K < 1 || N < 1 || !group_ok(group)) return MOE_ERR_INVALID_ARGUMENT;
+  if (K % 8 || N % 8 || K >= kMaxDim || N >= kMaxDim || E > kMaxExperts)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// The workspace of moe_w4_forward: h rows, slots, the shared expert's.
+struct W4Ws {
+  size_t h, hs, y, ys, total;
+};
+W4Ws w4_ws(const moe_shape* s) {
+  W4Ws w;
+  const size_t F = (size_t)(s->S * s->k);
+  size_t o = 0;
+  auto take = [&](size_t n) {
+    const size_t at = o;
+    o += ffn_round_up(n, 256);
+    return at;
+  };
+  w.h = take(F * s->D * 2);
+  w.y = take(F * s->H * 4);
+  w.hs = take((size_t)(s->S * s->D_shared) * 2);
+  w.ys = take(s->D_shared ? (size_t)(s->S * s->H) * 4 : 0);
+  w.total = o ? o : 256;
+  return w;
+}
+
+moe_status check_w4_layer(const moe_shape* s) {
+  if (s == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (s->dtype != MOE_F32 && s->dtype != MOE_BF16 && s->dtype != MOE_MXFP8)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (s->S < 0 || s->H < 1 || s->D < 1 || s->E < 1 || s->k < 1 || s->k > s->E ||
+      s->D_shared < 0 || s->capacity < 0)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (s->dtype != MOE_BF16 || s->capacity != 0 || (s->flags & ~MOE_OUTPUT_F32) != 0)
+    return MOE_ERR_UNSUPPORTED;
+  if (s->H % 8 || s->D % 8 || s->D_shared % 8 || s->H >= kMaxDim || s->D >= kMaxDim ||
+      s->D_shared >= kMaxDim || s->E > 1024 || s->k > 32 || s->S > kMaxRows ||
+      s->S * s->k > kMaxRows)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_w4_weight_bytes(int64_t E, int64_t K, int64_t N, int32_t group) {
+  if (check_w4(E, K, N, group) != MOE_OK) return 0;
+  return (size_t)E * tiles_n(N) * tiles_k(K) * tile_bytes(group);
+}
+
+extern "C" moe_status moe_quantize_w4(const void* W, int64_t E, int64_t K, int64_t N,
+                                      int32_t dtype, int32_t group, uint8_t* codes, void* scales,
+                                      void* stream) {
+  const moe_status st = check_w4(E, K, N, group);
+  if (st != MOE_OK) return st;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+  if (W == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  const int es = dtype == MOE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(W) % es || reinterpret_cast<uintptr_t>(scales) % 2)
+    return MOE_ERR_UNSUPPORTED;
+  const int64_t n = E * ((K + group - 1) / group) * N;
+  if ((n + 255) / 256 >= (1 << 24)) return MOE_ERR_UNSUPPORTED;  // a launch's 2^32 threads
+  const unsigned grid = (unsigned)((n + 255) / 256);
+  if (dtype == MOE_F32)
+    w4_quantize_kernel<<<grid, 256, 0, (hipStream_t)stream>>>((const float*)W, E, K, N, group,
+                                                              codes, (bf16_t*)scales);
+  else
+    w4_quantize_kernel<<<grid, 256, 0, (hipStream_t)stream>>>((const bf16_t*)W, E, K, N, group,
+                                                              codes, (bf16_t*)scales);
+  return enqueued();
+}
+
+extern "C" moe_status moe_pack_w4_weights(const uint8_t* codes, const void* scales, int64_t E,
+                                          int64_t K, int64_t N, int32_t group, void* packed,
+                                          void* stream) {
+  const moe_status st = check_w4(E, K, N, group);
+  if (st != MOE_OK) return st;
+  if (codes == nullptr || scales == nullptr || packed == nullptr ||
+      (const void*)codes == scales || packed == (const void*)codes || packed == scales)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!ffn_aligned16(packed) || reinterpret_cast<uintptr_t>(scales) % 2)
+    return MOE_ERR_UNSUPPORTED;
+  const int64_t tiles = E * tiles_n(N) * tiles_k(K);
+  if ((tiles + 3) / 4 >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  w4_pack_kernel<<<(unsigned)((tiles + 3) / 4), 256, 0, (hipStream_t)stream>>>(
+      codes, (const bf16_t*)scales, E, K, N, group, (char*)packed);
+  return enqueued();
+}
+
+extern "C" moe_status moe_w4_matvec(int64_t S, int64_t K, int64_t N, int64_t E, int32_t group,
+                                    int32_t flags, const void* X, const void* W,
+                                    const int32_t* expert_ids, void* Y, void* stream) {
+  if (S < 0 || (flags & ~MOE_OUTPUT_F32) != 0) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_status st = check_w4(E, K, N, group);
+  if (st != MOE_OK) return st;
+  if (S > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (S == 0) return MOE_OK;
+  if (X == nullptr || W == nullptr || Y == nullptr || X == Y || W == Y)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!ffn_aligned16(X) || !ffn_aligned16(W) || !ffn_aligned16(Y) ||
+      reinterpret_cast<uintptr_t>(expert_ids) % 4)
+    return MOE_ERR_UNSUPPORTED;
+  W4Args p = {};
+  p.X = (const bf16_t*)X;
+  p.w[0] = (const char*)W;
+  p.ids = expert_ids;
+  p.out = Y;
+  p.K = K;
+  p.N = N;
+  p.F = (int)S;
+  p.E = (int)E;
+  p.k = 1;
+  p.by_row = S <= E;
+  p.out_f32 = (flags & MOE_OUTPUT_F32) != 0;
+  const int64_t entries = expert_ids == nullptr ? (S + 15) / 16 : p.by_row ? S : E + 1;
+  if (entries * tiles_n(N) >= kMaxTiles) return MOE_ERR_UNSUPPORTED;
+  launch_w4<kMatvec>(group, p, entries, 0, (hipStream_t)stream);
+  return enqueued();
+}
+
+extern "C" size_t moe_w4_forward_workspace_bytes(const moe_shape* shape) {
+  return check_w4_layer(shape) == MOE_OK ? w4_ws(shape).total : 0;
+}
+
+extern "C" moe_status moe_w4_forward(const moe_shape* s, int32_t group, const void* A,
+                                     const void* W_up, const void* W_gate, const void* W_down,
+                                     const void* Ws_up, const void* Ws_gate, const void* Ws_down,
+                                     const int32_t* topk_ids, const float* topk_weights, void* O,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  const moe_status st = check_w4_layer(s);
+  if (st != MOE_OK) return st;
+  if (!group_ok(group)) return MOE_ERR_INVALID_ARGUMENT;
+  if (s->S == 0) return MOE_OK;
+  if (A == nullptr || W_up == nullptr || W_gate == nullptr || W_down == nullptr ||
+      topk_ids == nullptr || topk_weights == nullptr || O == nullptr || O == A)
+    return MOE_ERR_INVALID_ARGUMENT;
+  const bool sh = s->D_shared > 0;
+  if ((Ws_up != nullptr) != sh || (Ws_gate != nullptr) != sh || (Ws_down != nullptr) != sh)
+    return MOE_ERR_INVALID_ARGUMENT;
+  for (const void* q : {A, W_up, W_gate, W_down, Ws_up, Ws_gate, Ws_down, (const void*)O,
+                        (const void*)workspace})
+    if (!ffn_aligned16(q)) return MOE_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(topk_ids) % 4 || reinterpret_cast<uintptr_t>(topk_weights) % 4)
+    return MOE_ERR_UNSUPPORTED;
+  const W4Ws ws = w4_ws(s);
+  if (workspace == nullptr || workspace_bytes < ws.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  char* base = (char*)workspace;
+  hipStream_t stq = (hipStream_t)stream;
+  W4Args p = {};
+  p.F = (int)(s->S * s->k);
+  p.E = (int)s->E;
+  p.k = (int)s->k;
+  p.S = sh ? (int)s->S : 0;
+  p.ids = topk_ids;
+  p.by_row = p.F <= p.E;
+  const int64_t entries = p.by_row ? p.F : p.E, blocks_s = (p.S + 15) / 16;
+  const int64_t cols = tiles_n(s->D > s->H ? s->D : s->H);
+  const int64_t cols_s = tiles_n(s->D_shared > s->H ? s->D_shared : s->H);
+  if (entries * cols + blocks_s * cols_s >= kMaxTiles) return MOE_ERR_UNSUPPORTED;
+  // up, gate and SwiGLU
+  p.X = p.Xs = (const bf16_t*)A;
+  p.w[0] = (const char*)W_up;
+  p.w[1] = (const char*)W_gate;
+  p.ws[0] = (const char*)Ws_up;
+  p.ws[1] = (const char*)Ws_gate;
+  p.out = base + ws.h;
+  p.outs = base + ws.hs;
+  p.K = p.Ks = s->H;
+  p.N = s->D;
+  p.Ns = s->D_shared;
+  launch_w4<kUpgate>(group, p, entries, blocks_s, stq);
+  // down
+  p.X = (const bf16_t*)(base + ws.h);
+  p.Xs = (const bf16_t*)(base + ws.hs);
+  p.w[0] = (const char*)W_down;
+  p.ws[0] = (const char*)Ws_down;
+  p.out = base + ws.y;
+  p.outs = base + ws.ys;
+  p.K = s->D;
+  p.Ks = s->D_shared;
+  p.N = p.Ns = s->H;
+  launch_w4<kDown>(group, p, entries, blocks_s, stq);
+  const float* y = (const float*)(base + ws.y);
+  const float* ys = sh ? (const float*)(base + ws.ys) : nullptr;
+  const unsigned grid = (unsigned)((s->S * s->H / 4 + 255) / 256);
+  if (s->flags & MOE_OUTPUT_F32)
+    w4_combine_kernel<<<grid, 256, 0, stq>>>(s->S, s->H, p.k, p.E, topk_ids, topk_weights, y, ys,
+                                             (float*)O);
+  else
+    w4_combine_kernel<<<grid, 256, 0, stq>>>(s->S, s->H, p.k, p.E, topk_ids, topk_weights, y, ys,
+                                             (bf16_t*)O);
+  return enqueued();
+}

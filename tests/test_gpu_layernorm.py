@@ -1,0 +1,147 @@
+"""Layer norm, forward and backward, against 64-bit forms with derived bounds."""
+import pytest
+import torch
+
+import sparse_expert_ffn_amd as moe
+from sparse_expert_ffn_amd.layer import LayerNormBuffers
+from tests.ffn_util import DEV, check, gen, half, ln_bwd_ref, ln_ref, normal
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+MD = {BF: moe.MOE_BF16, F32: moe.MOE_F32}
+
+# one element, less than a vector, odd lengths, the edges of the wave and workgroup
+# kernels (bf16: 2048, 16384; fp32: 1024, 8192; element-wise: 512, 4096), longer rows
+SHAPES = [(1, 1), (5, 3), (64, 8), (3, 40), (7, 511), (9, 512), (4, 513), (130, 1001),
+          (33, 1024), (6, 1032), (17, 2048), (5, 2056), (3, 4097), (2, 8192), (3, 8200),
+          (2, 16384), (3, 16392), (2, 20001), (1, 65544), (3000, 72), (1025, 264)]
+
+
+def make(S, H, t, seed):
+    g = gen(seed)
+    off = torch.randn(H, generator=g, device=DEV) * 2
+    x = (torch.randn((S, H), generator=g, device=DEV) + off).to(t)
+    return x, normal(g, (H,), 0.2, t, 1.0), normal(g, (H,), 0.3, t), normal(g, (S, H), 0.5, t)
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("S,H", SHAPES)
+def test_forward_and_backward(S, H, t):
+    print(f"[layernorm {S}x{H} {t}]", flush=True)
+    x, gamma, beta, dy = make(S, H, t, 1)
+    b = LayerNormBuffers(S, H, MD[t], device=DEV)
+    b.ws.fill_(0xFF)
+    y = b.forward(x, gamma, beta, eps=1e-5)
+    ry, rm, rr, ey, em, er = ln_ref(x, gamma, beta, 1e-5)
+    check("mean", b.mean, rm, em)
+    check("rstd", b.rstd, rr, er)
+    check("y", y, ry, ey + half(t) * (ry.abs() + ey) + 1e-38)
+    dx, dg, db = b.backward(dy, x, gamma)
+    rx, rg, rb, ex, eg, eb = ln_bwd_ref(dy, x, gamma, b.mean, b.rstd)
+    check("dx", dx, rx, ex + half(t) * (rx.abs() + ex) + 1e-38)
+    check("dgamma", dg, rg, eg)
+    check("dbeta", db, rb, eb)
+    first = [v.clone() for v in (dx, dg, db)]
+    b.backward(dy, x, gamma)
+    assert all(torch.equal(p, q) for p, q in zip(first, (dx, dg, db))), "not reproducible"
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+def test_without_weights_and_statistics(t):
+    x, _, _, dy = make(50, 264, t, 2)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    moe.moe_layernorm_forward(x, None, None, 1e-3, y)
+    ry, rm, rr, ey, _, _ = ln_ref(x, None, None, 1e-3)
+    check("y", y, ry, ey + half(t) * (ry.abs() + ey))
+    mean, rstd = rm.float(), rr.float()
+    moe.moe_layernorm_backward(dy, x, None, mean, rstd, dx, None, None, None)
+    rx, _, _, ex, _, _ = ln_bwd_ref(dy, x, None, mean, rstd)
+    check("dx", dx, rx, ex + half(t) * (rx.abs() + ex))
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H", [64, 2056, 20000])
+def test_arrays_off_16_bytes(t, H):
+    """Bases that only an element's alignment holds for give the vector path's values."""
+    S = 5
+    x, gamma, beta, dy = make(S, H, t, 3)
+
+    def shifted(v):
+        s = torch.empty(v.numel() + 1, dtype=v.dtype, device=DEV)[1:].view(v.shape)
+        return s.copy_(v)
+
+    y = shifted(torch.zeros_like(x))
+    mean, rstd = torch.empty(S, device=DEV), torch.empty(S, device=DEV)
+    moe.moe_layernorm_forward(shifted(x), shifted(gamma), shifted(beta), 1e-5, y, mean, rstd)
+    ry, rm, rr, ey, em, er = ln_ref(x, gamma, beta, 1e-5)
+    check("y", y, ry, ey + half(t) * (ry.abs() + ey))
+    dx = shifted(torch.zeros_like(x))
+    dg, db = torch.empty(H, device=DEV), torch.empty(H, device=DEV)
+    ws = torch.empty(moe.moe_layernorm_backward_workspace_bytes(S, H, MD[t]), dtype=torch.uint8,
+                     device=DEV)
+    moe.moe_layernorm_backward(shifted(dy), shifted(x), shifted(gamma), mean, rstd, dx, dg, db,
+                               ws)
+    rx, rg, rb, ex, eg, eb = ln_bwd_ref(dy, x, gamma, mean, rstd)
+    check("dx", dx, rx, ex + half(t) * (rx.abs() + ex))
+    check("dgamma", dg, rg, eg)
+    check("dbeta", db, rb, eb)
+
+
+def test_large_offset_keeps_the_variance():
+    """Rows of 4096 + noise: the squares are centred before they are summed."""
+    g = gen(4)
+    x = torch.randn((8, 1024), generator=g, device=DEV) * 0.5 + 4096
+    y = torch.empty_like(x)
+    moe.moe_layernorm_forward(x, None, None, 0.0, y)
+    ry, _, _, ey, _, _ = ln_ref(x, None, None, 0.0)
+    check("y", y, ry, ey + half(F32) * ry.abs())
+    assert float(ey.max()) < 0.1  # the bound says something
+
+
+def test_constant_rows_and_not_finite_rows():
+    x = torch.ones((4, 512), device=DEV)
+    x[1, 7] = float("inf")
+    x[2, 0] = float("nan")
+    y = torch.empty_like(x)
+    moe.moe_layernorm_forward(x, None, None, 1e-5, y)
+    assert torch.equal(y[0], torch.zeros(512, device=DEV)) and torch.equal(y[3], y[0])
+    assert bool(torch.isnan(y[1]).any()) and bool(torch.isnan(y[2]).all())
+
+
+def test_no_rows():
+    for t in (BF, F32):
+        x = torch.empty((0, 64), dtype=t, device=DEV)
+        b = LayerNormBuffers(0, 64, MD[t], device=DEV)
+        b.dgamma.fill_(7)
+        b.dbeta.fill_(7)
+        b.forward(x)
+        b.backward(x, x)
+        assert float(b.dgamma.abs().max()) == 0 and float(b.dbeta.abs().max()) == 0
+
+
+def test_gradient_against_differences():
+    """Along a random direction v: (L(x + e v) - L(x - e v)) / 2 e = <dx, v> for L =
+    sum c y, the differences taken in 64 bits."""
+    g = gen(5)
+    S, H = 6, 96
+    x = torch.randn((S, H), generator=g, device=DEV)
+    gamma = torch.randn(H, generator=g, device=DEV)
+    c = torch.randn((S, H), generator=g, device=DEV)
+    v = torch.randn((S, H), generator=g, device=DEV).double()
+    b = LayerNormBuffers(S, H, moe.MOE_F32, device=DEV)
+    b.forward(x, gamma)
+    dx, dg, db = b.backward(c, x, gamma)
+
+    def loss(z, gm):
+        m = z.mean(1, keepdim=True)
+        return float((c.double() * ((z - m) / ((z - m).square().mean(1, keepdim=True) + 1e-5)
+                                    .sqrt() * gm)).sum())
+
+    e = 1e-4  # the difference's own error is e^2 = 1e-8 of third derivatives of order 10
+    num = (loss(x.double() + e * v, gamma.double()) - loss(x.double() - e * v, gamma.double())) \
+        / (2 * e)
+    assert abs(num - float((dx.double() * v).sum())) < 1e-4
+    w = v[0]
+    num = (loss(x.double(), gamma.double() + e * w) - loss(x.double(), gamma.double() - e * w)) \
+        / (2 * e)
+    assert abs(num - float((dg.double() * w).sum())) < 1e-4
