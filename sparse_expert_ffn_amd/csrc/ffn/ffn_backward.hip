@@ -59,7 +59,7 @@ void backward_t(const moe_ffn_shape* s, const BwdPlan& p, const void* dO, const 
     g.N = s->H;
     g.K[0] = g.K[1] = s->D;
     apply_plan(p.dx, &g, ws + p.part);
-    launch_gemm<T, false, true, true>(p.dx, g, EpStore<T>{(T*)dX, s->H}, st);
+    launch_gemm<T, false, true, true>(p.dx, g, EpStore<T>{(T*)dX, nullptr, s->H}, st);
   }
   if (dWu != nullptr) {
     g = GemmArgs{};
@@ -73,7 +73,7 @@ void backward_t(const moe_ffn_shape* s, const BwdPlan& p, const void* dO, const 
     g.N = s->D;
     g.K[0] = s->S;
     apply_plan(p.dw, &g, ws + p.part);
-    launch_gemm<T, true, false, false>(p.dw, g, EpStore2<TW>{(TW*)dWu, (TW*)dWg, s->D}, st);
+    launch_gemm<T, true, false, false>(p.dw, g, EpStore<TW, true>{(TW*)dWu, (TW*)dWg, s->D}, st);
     g.A[0] = h;
     g.B[0][0] = dO;
     g.lda = s->D;
@@ -81,7 +81,7 @@ void backward_t(const moe_ffn_shape* s, const BwdPlan& p, const void* dO, const 
     g.M = s->D;
     g.N = s->H;
     apply_plan(p.dwd, &g, ws + p.part);
-    launch_gemm<T, false, false, false>(p.dwd, g, EpStore<TW>{(TW*)dWd, s->H}, st);
+    launch_gemm<T, false, false, false>(p.dwd, g, EpStore<TW>{(TW*)dWd, nullptr, s->H}, st);
   }
 }
 

@@ -52,9 +52,9 @@ void forward_t(const moe_ffn_shape* s, const FwdPlan& p, const void* X, const vo
   g.K[0] = s->D;
   apply_plan(p.down, &g, ws + p.part);
   if (s->flags & MOE_OUTPUT_F32)
-    launch_gemm<T, false, true, false>(p.down, g, EpStore<float>{(float*)O, s->H}, st);
+    launch_gemm<T, false, true, false>(p.down, g, EpStore<float>{(float*)O, nullptr, s->H}, st);
   else
-    launch_gemm<T, false, true, false>(p.down, g, EpStore<T>{(T*)O, s->H}, st);
+    launch_gemm<T, false, true, false>(p.down, g, EpStore<T>{(T*)O, nullptr, s->H}, st);
 }
 }  // namespace
 

@@ -9,20 +9,21 @@
 // their gradients), and K may run over two pairs of operands in turn (dX = dU
 // W_up^T + dG W_gate^T).
 //
-// bf16 (BfCore): K stages of 64 go from global memory straight into a ring of
-// LDS slots (16 bytes per lane). KC operands lie there as rows of 128 bytes and
-// are read by ds_read_b128, MC operands as K rows of a panel of up to 128
-// columns and are read transposed (ds_read_b64_tr_b16); both with the chunk
-// orders that the MoE layer's tile core measured free of bank conflicts. The MFMA
-// takes B's fragment as its first operand, so a lane ends up with 4 consecutive
-// columns of one row and loads and stores them as one access.
+// K stages of 128 bytes (64 bf16, 32 fp32) go from global memory straight into a
+// ring of LDS slots (16 bytes per lane). KC operands lie there as rows of 128
+// bytes and are read 16 bytes per lane, MC operands as K rows of a panel of up to
+// 256 bytes and are read transposed (bf16: ds_read_b64_tr_b16; fp32: 4 bytes per
+// lane), in the chunk orders that the MoE layer's tile core measured free of
+// bank conflicts (fp32 MC: 64-byte units ordered by the lane group).
+//   bf16: v_mfma_f32_16x16x32_bf16, a lane's 16 bytes are 8 K values of a row;
+//   fp32: four v_mfma_f32_16x16x4_f32, a lane's 16 bytes are 4 K values, one per
+//         MFMA: any order of K serves that is the same for both operands.
+// The MFMA takes B's fragment as its first operand, so a lane ends up with 4
+// consecutive columns of one row and loads and stores them as one access.
 //
 // The operands are addressed from a base that moves along K with the stages
 // (scalar arithmetic), so an array may exceed the 4 GiB of a buffer's range;
 // out-of-range rows, columns and K values read as zeros.
-//
-// fp32 (F32Core): the same interface on v_mfma_f32_16x16x4_f32; the 32x slower
-// matrix rate leaves time for staging through registers.
 #pragma once
 
 #include "ffn_common.h"
@@ -56,103 +57,135 @@ __device__ __forceinline__ i32x4_t window_srd(uint64_t base, int64_t left) {
   return r;
 }
 
-// One operand (R tile rows or columns in panels of PW, NB bases) in LDS.
-template <bool KC, int R, int PW, int BASES, int NW>
-struct BfOperand {
-  static constexpr int BK = 64;
-  static constexpr int BYTES = R * BK * 2;
+// One operand (R tile rows or columns in panels of PW, with one or two bases) in LDS.
+//
+// KC: row r at r * 128 bytes, its 16-byte chunk c in slot c ^ (r / 2) % 8.
+// MC: panel by panel, K row k of a panel at k * ROWB bytes; its units (32 bytes in
+// bf16, 64 in fp32: 16 columns) u in slot u ^ swz_mc(k).
+template <typename T, bool KC, int R, int PW, int BASES, int NW>
+struct Operand {
+  static constexpr int ES = sizeof(T);
+  static constexpr int BK = 128 / ES;          // K values per stage
+  static constexpr int BYTES = R * 128;        // per stage
   static constexpr int INSTR = BYTES / 1024;
   static constexpr int PER_WAVE = (INSTR + NW - 1) / NW;
-  static constexpr int PANEL_INSTR = PW * BK * 2 / 1024;
-  static_assert(KC || PW == 64 || PW == 128, "panel width");
+  static constexpr int PANEL = PW * 128;       // bytes per panel and stage
+  static constexpr int PANEL_INSTR = PANEL / 1024;
+  static constexpr int ROWB = PW * ES;         // MC: bytes per K row of a panel
+  static constexpr int CPU = ES;               // MC: 16-byte chunks per 16-column unit
+  static_assert(KC || ROWB == 128 || ROWB == 256, "panel width");
   static_assert(INSTR % NW == 0 || INSTR < NW, "loads split evenly");
-  static_assert(BASES == 1 || (PANEL_INSTR % NW == 0) || KC || PW == 64, "panels");
 
+  int wave;
   uint32_t off[PER_WAVE];
+  int chunk_k;           // KC: this lane's K value within a stage, for all its loads
   uint64_t base[BASES];
   int64_t left[BASES];   // bytes from base to the operand's end
   int64_t step;          // bytes per stage
+  i32x4_t srd[BASES];    // of the next stage to load
+  uint32_t rd[2];        // LDS offset of this lane's fragment reads (KC: per K step)
 
   __device__ __forceinline__ static int swz_kc(int r) { return (r >> 1) & 7; }
   __device__ __forceinline__ static int swz_mc(int k) {
-    return PW == 128 ? (k & 3) | (((k >> 3) & 1) << 2) : ((k >> 1) & 1) | (((k >> 3) & 1) << 1);
+    if (ES == 4) return (k >> 2) & (ROWB == 256 ? 3 : 1);
+    return ROWB == 256 ? (k & 3) | (((k >> 3) & 1) << 2) : ((k >> 1) & 1) | (((k >> 3) & 1) << 1);
   }
 
-  // Tile rows (columns) r0 + p * panel_stride .. of panel p; n valid in all.
-  __device__ __forceinline__ void setup(int64_t ld, int64_t r0, int64_t n, bool dual) {
+  // Tile rows (columns) from r0 on, n valid in all; with two bases each panel
+  // covers the same ones. w0: the first row (column) of each panel that this
+  // wave's fragments cover.
+  __device__ __forceinline__ void setup(int wave_, int64_t ld, int64_t r0, int64_t n, int w0) {
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    step = KC ? BK * 2 : (int64_t)BK * ld * 2;
+    wave = wave_;
+    step = KC ? 128 : (int64_t)BK * ld * ES;
 #pragma unroll
     for (int t = 0; t < PER_WAVE; ++t) {
       const int q = wave + NW * t;
       if constexpr (KC) {
         const int r = q * 8 + (lane >> 3);
+        // the chunk is the same for every t (rows 8 NW apart, or one load only)
         const int c = (lane & 7) ^ swz_kc(r);
-        const int rr = dual ? r % PW : r;
-        off[t] = r0 + rr < n ? (uint32_t)(rr * ld * 2 + c * 16) : kOutOfRange;
+        const int rr = BASES == 2 ? r % PW : r;
+        chunk_k = c * (16 / ES);
+        off[t] = r0 + rr < n ? (uint32_t)(rr * ld * ES + c * 16) : kOutOfRange;
       } else {
-        constexpr int CH = PW / 8;  // chunks per K row
+        constexpr int CH = ROWB / 16;  // chunks per K row
         const int kr = (q % PANEL_INSTR) * (64 / CH) + lane / CH;
         const int pc = lane % CH;
-        const int c = (((pc >> 1) ^ swz_mc(kr)) << 1) | (pc & 1);
-        const int col = (dual ? 0 : q / PANEL_INSTR * PW) + c * 8;
-        off[t] = r0 + col < n ? (uint32_t)(kr * ld * 2 + col * 2) : kOutOfRange;
+        const int c = (pc / CPU ^ swz_mc(kr)) * CPU + pc % CPU;
+        const int col = (BASES == 2 ? 0 : q / PANEL_INSTR * PW) + c * (16 / ES);
+        off[t] = r0 + col < n ? (uint32_t)(kr * ld * ES + col * ES) : kOutOfRange;
       }
+    }
+    const int lr = lane & 15, lg = lane >> 4;
+    if constexpr (KC) {
+      rd[0] = (w0 + lr) * 128 + ((lg ^ swz_kc(lr)) << 4);
+      rd[1] = (w0 + lr) * 128 + (((4 + lg) ^ swz_kc(lr)) << 4);
+    } else if constexpr (ES == 2) {
+      // K row 8 lg + lr / 4 of a step (+ 4 for the second read), 4 columns at
+      // 4 (lr % 4) of a 16-column block: block j of the wave at rd ^ (j * 32)
+      const int k = 8 * lg + (lr >> 2);
+      rd[0] = w0 / PW * PANEL + k * ROWB + ((w0 % PW / 16 ^ swz_mc(k)) << 5) + ((lr & 3) << 3);
+    } else {
+      // K rows 4 lg .. + 3 of a step, column lr of block j at rd ^ (j * 64)
+      rd[0] = w0 / PW * PANEL + 4 * lg * ROWB + ((w0 % PW / 16 ^ swz_mc(4 * lg)) << 6) + lr * 4;
     }
   }
   // Base `b` of an operand at p, of n rows (columns), K values, at K value k0.
   __device__ __forceinline__ void seek(int b, const void* p, int64_t ld, int64_t r0, int64_t n,
                                        int64_t K, int64_t k0) {
-    const int64_t at = KC ? (r0 * ld + k0) * 2 : (k0 * ld + r0) * 2;
+    const int64_t at = KC ? (r0 * ld + k0) * ES : (k0 * ld + r0) * ES;
     base[b] = reinterpret_cast<uint64_t>(p) + (uint64_t)at;
-    left[b] = (KC ? n * ld : K * ld) * 2 - at;
+    left[b] = (KC ? n * ld : K * ld) * ES - at;
+    srd[b] = window_srd(base[b], left[b]);
   }
   __device__ __forceinline__ void advance() {
 #pragma unroll
     for (int b = 0; b < BASES; ++b) {
       base[b] += (uint64_t)step;
       left[b] -= step;
+      srd[b] = window_srd(base[b], left[b]);
+    }
+  }
+  // From here on loads give zeros.
+  __device__ __forceinline__ void close() {
+#pragma unroll
+    for (int b = 0; b < BASES; ++b) {
+      left[b] = 0;
+      srd[b].z = 0;
     }
   }
   // This wave's load t of the stage; kleft: K values from the stage's first on.
   __device__ __forceinline__ void issue(char* lds, int t, int kleft) const {
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = wave + NW * t;
     if (INSTR % NW != 0 && q >= INSTR) return;
     int b = 0;
-    if constexpr (BASES == 2) b = q / PANEL_INSTR;
-    const i32x4_t srd = b == 0 ? window_srd(base[0], left[0])
-                               : window_srd(base[BASES - 1], left[BASES - 1]);
+    if constexpr (BASES == 2) b = PANEL_INSTR % NW == 0 ? NW * t / PANEL_INSTR : q / PANEL_INSTR;
+    const i32x4_t r = b == 0 ? srd[0] : srd[BASES - 1];
     uint32_t o = off[t];
-    if constexpr (KC) {
-      const int c = (lane & 7) ^ swz_kc(q * 8 + (lane >> 3));
-      o = c * 8 < kleft ? o : kOutOfRange;
-    }
-    dma16<true>(srd, o, lds + q * 1024);
+    if constexpr (KC) o = chunk_k < kleft ? o : kOutOfRange;
+    dma16(r, o, lds + q * 1024);
   }
-  // Fragment of the 16 rows (columns) at r (a multiple of 16) for K step ks of 32.
-  __device__ __forceinline__ static uint4 frag(const char* lds, int r, int ks) {
-    const int lane = threadIdx.x & 63;
-    const int lr = lane & 15, lg = lane >> 4;
+  // Fragment of the wave's 16-row (column) block j of panel p for K step ks. MC: a
+  // wave's blocks lie in one panel and start at a multiple of their number, so
+  // that the exclusive or adds j.
+  __device__ __forceinline__ uint4 frag(const char* lds, int p, int j, int ks) const {
     if constexpr (KC) {
-      const int row = r + lr;
-      return *reinterpret_cast<const uint4*>(lds + row * 128 +
-                                             (((ks * 4 + lg) ^ swz_kc(row)) << 4));
-    } else {
+      return *reinterpret_cast<const uint4*>(lds + rd[ks] + (p * PW + j * 16) * 128);
+    } else if constexpr (ES == 2) {
       i16x4_t h[2];
+      const char* q = lds + (rd[0] ^ (uint32_t)(j << 5)) + p * PANEL + ks * 32 * ROWB;
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int k = ks * 32 + 8 * lg + 4 * hh + (lr >> 2);
-        const int n = r + 4 * (lr & 3);
-        const int c = (n % PW) >> 3;
-        const int pc = (((c >> 1) ^ swz_mc(k)) << 1) | (c & 1);
-        const char* p = lds + n / PW * (PW * BK * 2) + k * (PW * 2) + (pc << 4) + ((n & 4) << 1);
+      for (int hh = 0; hh < 2; ++hh)
         h[hh] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) i16x4_t*)(p));
-      }
+            (__attribute__((address_space(3))) i16x4_t*)(q + 4 * hh * ROWB));
       return __builtin_bit_cast(uint4, h);
+    } else {
+      const char* q = lds + (rd[0] ^ (uint32_t)(j << 6)) + p * PANEL + ks * 16 * ROWB;
+      f32x4_t v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const float*>(q + e * ROWB);
+      return __builtin_bit_cast(uint4, v);
     }
   }
 };
@@ -160,16 +193,17 @@ struct BfOperand {
 // BM x BN tile by WM x WN waves, NP column panels of BN / NP, DUAL: each panel
 // has a B and a C of its own. A wave covers the same BN / NP / WN columns of each
 // panel. NST: LDS slots.
-template <int BM_, int BN_, int NP_, bool DUAL_, bool AKC, bool BKC, int WM, int WN, int NST_>
-struct BfCore {
-  using elem = bf16_t;
-  static constexpr int BM = BM_, BN = BN_, NP = NP_, BK = 64, NST = NST_;
+template <typename T, int BM_, int BN_, int NP_, bool DUAL_, bool AKC, bool BKC, int WM, int WN,
+          int NST_>
+struct TileCore {
+  static constexpr int BM = BM_, BN = BN_, NP = NP_, BK = 128 / (int)sizeof(T), NST = NST_;
   static constexpr bool DUAL = DUAL_;
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int PWB = BN / NP;
-  static constexpr int PWA = AKC ? BM : (BM < 128 ? BM : 128);
-  using OpA = BfOperand<AKC, BM, PWA, 1, NW>;
-  using OpB = BfOperand<BKC, BN, PWB, DUAL ? 2 : 1, NW>;
+  static constexpr int PMAX = 256 / (int)sizeof(T);
+  static constexpr int PWA = AKC ? BM : (BM < PMAX ? BM : PMAX);
+  using OpA = Operand<T, AKC, BM, PWA, 1, NW>;
+  using OpB = Operand<T, BKC, BN, PWB, DUAL ? 2 : 1, NW>;
   static constexpr int MI = BM / WM / 16;
   static constexpr int NIP = PWB / WN / 16;  // 16-column blocks per wave and panel
   static constexpr int NI = NP * NIP;
@@ -179,6 +213,8 @@ struct BfCore {
   static constexpr int MIN_PW = OpA::INSTR / NW + OpB::INSTR / NW;
   static constexpr int PIECES = OpA::PER_WAVE + OpB::PER_WAVE;
   static_assert(MI >= 1 && NIP >= 1, "tile too small for the waves");
+  static_assert(AKC || (PWA % (BM / WM) == 0 && (MI & (MI - 1)) == 0), "A blocks in one panel");
+  static_assert(BKC || (NIP & (NIP - 1)) == 0, "B blocks");
   static_assert(LDS_BYTES <= 160 * 1024, "LDS");
   static_assert((NST - 1) * PIECES < 64, "vmcnt range");
 
@@ -212,227 +248,141 @@ struct BfCore {
     }
   }
 
-  template <typename Between>
-  __device__ __forceinline__ void compute(const char* slot, Between between) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm0 = wave / WN * (BM / WM);
-    const int wn0 = wave % WN * (PWB / WN);
+  uint4 fa[2][MI], fb[2][NI];  // fragments of two K steps of 32 in turn
+
+  // Fragment n of K step ks (B's column blocks, then A's row blocks) into set `to`.
+  __device__ __forceinline__ void read_frag(const char* slot, int ks, int to, int n) {
+    if (n < NI)
+      fb[to][n] = b.frag(slot + OpA::BYTES, n / NIP, n % NIP, ks);
+    else
+      fa[to][n - NI] = a.frag(slot, 0, n - NI, ks);
+  }
+
+  // The MFMAs of the K step in set `cur`, row block by row block; between them go
+  // the LDS reads of the next K step (from rd, into the other set; all of them out
+  // two row blocks before the end, so that they have landed when it starts) and,
+  // with `issue`, the global loads of a later stage into wr.
+  __device__ __forceinline__ void phase(int cur, const char* rd, int rd_ks, char* wr,
+                                        bool issue) {
+    constexpr int FRAGS = NI + MI;
+    constexpr int ROWS = MI > 2 ? MI - 1 : MI;  // row blocks that carry reads
+    constexpr int IROWS = MI < 4 ? MI : 4;      // and global loads
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      uint4 fb[NI], fa[MI];
+    for (int i = 0; i < MI; ++i) {
 #pragma unroll
-      for (int j = 0; j < NI; ++j)
-        fb[j] = OpB::frag(slot + OpA::BYTES, j / NIP * PWB + wn0 + j % NIP * 16, ks);
+      for (int e = 0; e < (sizeof(T) == 4 ? 4 : 1); ++e)
 #pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = OpA::frag(slot, wm0 + i * 16, ks);
+        for (int j = 0; j < NI; ++j) {
+          if constexpr (sizeof(T) == 4)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                __builtin_bit_cast(f32x4_t, fb[cur][j])[e],
+                __builtin_bit_cast(f32x4_t, fa[cur][i])[e], acc[i][j], 0, 0, 0);
+          else
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8_t, fb[cur][j]),
+                __builtin_bit_cast(bf16x8_t, fa[cur][i]), acc[i][j], 0, 0, 0);
+        }
+      if (i < ROWS) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8_t, fb[j]), __builtin_bit_cast(bf16x8_t, fa[i]),
-              acc[i][j], 0, 0, 0);
-        between(ks * MI + i);
+        for (int n = i * FRAGS / ROWS; n < (i + 1) * FRAGS / ROWS; ++n)
+          read_frag(rd, rd_ks, cur ^ 1, n);
       }
+      if (issue)
+#pragma unroll
+        for (int n = i * PIECES / IROWS; n < (i + 1) * PIECES / IROWS && n < PIECES; ++n)
+          issue_piece(wr, n);
+      __builtin_amdgcn_sched_barrier(0);  // the order of the row blocks stands
     }
   }
 
-  // K stages [s0, s0 + ns) of the tile at (m0, n0).
+  // K stages [s0, s0 + ns) of the tile at (m0, n0). All NST slots are in flight.
+  // Stage kt: its first K step's fragments were read during the previous phase;
+  // phase 0 reads the second K step's; then every wave's reads of the slot are done
+  // and stage kt + 1 has landed (one wait and barrier), and phase 1 reads stage
+  // kt + 1's first fragments and loads stage kt + NST into stage kt's slot.
   __device__ __forceinline__ void run(const GemmArgs& g, char* lds, int64_t m0, int64_t n0,
                                       int s0, int ns) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NI; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    a.setup(g.lda, m0, g.M, false);
-    b.setup(g.ldb, n0, g.N, DUAL);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    a.setup(wave, g.lda, m0, g.M, wave / WN * (BM / WM));
+    b.setup(wave, g.ldb, n0, g.N, wave % WN * (PWB / WN));
     const int first = (int)((g.K[0] + BK - 1) / BK);  // stages of pair 0
     pair = s0 < first ? 0 : 1;
     seek(g, m0, n0, (int64_t)(s0 - (pair ? first : 0)) * BK);
-    // issue stages behind the last one as zeros: the window ends there
     int to_issue = ns;
     auto finish = [&] {
       next_stage(g, m0, n0);
-      if (--to_issue <= 0) {
+      if (--to_issue <= 0) {  // stages past the last one load nothing (zeros)
         kleft = 0;
-        pair = 1 << 20;
-        a.left[0] = b.left[0] = 0;
-        if constexpr (DUAL) b.left[1] = 0;
+        pair = 2;
+        a.close();
+        b.close();
       }
     };
 #pragma unroll
-    for (int s = 0; s + 1 < NST; ++s) {
+    for (int s = 0; s < NST; ++s) {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) issue_piece(lds + s * STAGE, i);
       finish();
     }
-    int slot = 0, slot_next = NST - 1;
+    wait_vmcnt<(NST - 1) * MIN_PW>();
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NI + MI; ++n) read_frag(lds, 0, 0, n);
+    int slot = 0;
     for (int kt = 0; kt < ns; ++kt) {
+      char* cur = lds + slot * STAGE;
+      slot = slot + 1 == NST ? 0 : slot + 1;
+      phase(0, cur, 1, nullptr, false);
       wait_vmcnt<(NST - 2) * MIN_PW>();
       __syncthreads();
-      char* nxt = lds + slot_next * STAGE;
-      compute(lds + slot * STAGE, [&](int i) {
-        if (i < PIECES) issue_piece(nxt, i);
-      });
-#pragma unroll
-      for (int i = 2 * MI; i < PIECES; ++i) issue_piece(nxt, i);
+      __builtin_amdgcn_sched_barrier(0);
+      phase(1, lds + slot * STAGE, 0, cur, true);
       finish();
-      slot = slot + 1 == NST ? 0 : slot + 1;
-      slot_next = slot_next + 1 == NST ? 0 : slot_next + 1;
+      __builtin_amdgcn_sched_barrier(0);
     }
     wait_vmcnt<0>();
   }
 
-  // f(row, column, values of panel 0 .. of 4 consecutive columns): DUAL: one call
-  // with both panels' values of the same columns; else v1 is unused.
-  template <typename F>
-  __device__ __forceinline__ void for_each4(F f) const {
-    const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
-    const int row = wave / WN * (BM / WM) + (lane & 15);
-    const int col = wave % WN * (PWB / WN) + (lane >> 4) * 4;
+  // Consecutive columns of one row that a lane handles in the epilogue: the MFMA
+  // leaves 4; in bf16 two neighbouring blocks swap lane rows to make it 8, one
+  // 16-byte access.
+  static constexpr int W = sizeof(T) == 2 && NIP % 2 == 0 ? 8 : 4;
+  static constexpr int BPG = W / 4;            // blocks per group of W columns
+  static constexpr int GROUPS = (DUAL ? NIP : NI) / BPG;  // per row block
+
+  // Tile row and (panel's) column of group q of row block i.
+  __device__ __forceinline__ int group_row(int i) const {
+    return (threadIdx.x >> 6) / WN * (BM / WM) + i * 16 + (threadIdx.x & 15);
+  }
+  __device__ __forceinline__ int group_col(int q) const {
+    const int lg = (threadIdx.x & 63) >> 4;
+    const int j = q * BPG;
+    const int c = j / NIP * PWB + (threadIdx.x >> 6) % WN * (PWB / WN) + j % NIP * 16;
+    return W == 8 ? c + (lg & 1) * 16 + (lg >> 1) * 8 : c + lg * 4;
+  }
+  // Its values (of panel 1 with p = 1 in a DUAL tile).
+  __device__ __forceinline__ void group_values(int i, int q, int p, float (&v)[W]) {
+    const int j = p * NIP + q * BPG;
+    if constexpr (W == 8) {
+      // lane rows 0..3 hold columns 0, 4, 8, 12 and up of both blocks; after odd rows of
+      // the first swapped places with even rows of the second, row 0 holds the first
+      // block's columns 0..7, row 1 the second's, row 2 the first's 8..15, row 3 the
+      // second's
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      if constexpr (DUAL) {
-#pragma unroll
-        for (int j = 0; j < NIP; ++j)
-          f(row + i * 16, col + j * 16, acc[i][j], acc[i][NIP + j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-          f(row + i * 16, j / NIP * PWB + col + j % NIP * 16, acc[i][j], acc[i][j]);
+      for (int r = 0; r < 4; ++r) {
+        const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][r]),
+                                                        __float_as_uint(acc[i][j + 1][r]),
+                                                        false, false);
+        v[r] = __uint_as_float(w[0]);
+        v[4 + r] = __uint_as_float(w[1]);
       }
-    }
-  }
-};
-
-// fp32: 4 waves (2 x 2), K stages of 16 through registers into two LDS slots of
-// [16][rows + 4] floats per operand.
-template <int BM_, int BN_, int NP_, bool DUAL_, bool AKC, bool BKC>
-struct F32Core {
-  using elem = float;
-  static constexpr int BM = BM_, BN = BN_, NP = NP_, BK = 16;
-  static constexpr bool DUAL = DUAL_;
-  static constexpr int WM = 2, WN = 2, NW = 4, THREADS = 256;
-  static constexpr int PWB = BN / NP;
-  static constexpr int MI = BM / WM / 16, NIP = PWB / WN / 16, NI = NP * NIP;
-  static constexpr int PA = BM + 4, PB = BN + 4;
-  static constexpr int STAGE = BK * (PA + PB) * 4;
-  static constexpr int LDS_BYTES = 2 * STAGE;
-  static constexpr int LA = BM * BK / 4 / THREADS, LB = BN * BK / 4 / THREADS;
-  static_assert(LA >= 1 && LB >= 1 && MI >= 1 && NIP >= 1, "tile too small");
-
-  f32x4_t acc[MI][NI];
-  f32x4_t ra[LA], rb[LB];
-  int pair;
-  int64_t k;  // of the next stage to load, within the pair
-
-  template <bool KC, int R>
-  __device__ __forceinline__ static f32x4_t load(const float* p, int64_t ld, int64_t r0,
-                                                 int64_t n, int64_t K, int64_t k0, int idx) {
-    f32x4_t z = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (KC) {
-      const int64_t r = r0 + idx / 4, kk = k0 + idx % 4 * 4;
-      return r < n && kk < K ? load4(p + r * ld + kk) : z;
     } else {
-      const int64_t kk = k0 + idx / (R / 4), r = r0 + idx % (R / 4) * 4;
-      return r < n && kk < K ? load4(p + kk * ld + r) : z;
-    }
-  }
-  template <bool KC, int R, int P>
-  __device__ __forceinline__ static void put(float* lds, int idx, f32x4_t v) {
-    if constexpr (KC) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) lds[(idx % 4 * 4 + e) * P + idx / 4] = v[e];
-    } else {
-      store4(lds + idx / (R / 4) * P + idx % (R / 4) * 4, v);
-    }
-  }
-  __device__ __forceinline__ void fetch(const GemmArgs& g, int64_t m0, int64_t n0) {
-    const float* A = (const float*)g.A[pair];
-#pragma unroll
-    for (int t = 0; t < LA; ++t)
-      ra[t] = load<AKC, BM>(A, g.lda, m0, g.M, g.K[pair], k, threadIdx.x + t * THREADS);
-    // an index of B runs over panels of PWB rows (columns)
-#pragma unroll
-    for (int t = 0; t < LB; ++t) {
-      const int idx = threadIdx.x + t * THREADS;
-      constexpr int PER = PWB * BK / 4;
-      const int p = idx / PER;
-      rb[t] = load<BKC, PWB>((const float*)(DUAL && p ? g.B[pair][1] : g.B[pair][0]), g.ldb,
-                             n0 + (DUAL ? 0 : p * PWB), g.N, g.K[pair], k, idx % PER);
-    }
-    k += BK;
-    if (k >= g.K[pair] && pair + 1 < g.pairs) {
-      ++pair;
-      k = 0;
-    }
-  }
-  __device__ __forceinline__ void stage(float* lds) const {
-#pragma unroll
-    for (int t = 0; t < LA; ++t) put<AKC, BM, PA>(lds, threadIdx.x + t * THREADS, ra[t]);
-#pragma unroll
-    for (int t = 0; t < LB; ++t) {
-      const int idx = threadIdx.x + t * THREADS;
-      constexpr int PER = PWB * BK / 4;
-      put<BKC, PWB, PB>(lds + BK * PA + idx / PER * PWB, idx % PER, rb[t]);
-    }
-  }
-  __device__ __forceinline__ void compute(const float* lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int lr = lane & 15, lg = lane >> 4;
-    const int wm0 = wave / WN * (BM / WM), wn0 = wave % WN * (PWB / WN);
-#pragma unroll
-    for (int ks = 0; ks < BK / 4; ++ks) {
-      float fa[MI], fb[NI];
-      const int kk = ks * 4 + lg;
-#pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = lds[kk * PA + wm0 + i * 16 + lr];
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-        fb[j] = lds[BK * PA + kk * PB + j / NIP * PWB + wn0 + j % NIP * 16 + lr];
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    }
-  }
-  __device__ __forceinline__ void run(const GemmArgs& g, char* lds, int64_t m0, int64_t n0,
-                                      int s0, int ns) {
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    const int first = (int)((g.K[0] + BK - 1) / BK);
-    pair = s0 < first ? 0 : 1;
-    k = (int64_t)(s0 - (pair ? first : 0)) * BK;
-    fetch(g, m0, n0);
-    for (int kt = 0; kt < ns; ++kt) {
-      float* slot = reinterpret_cast<float*>(lds + (kt & 1) * STAGE);
-      stage(slot);
-      if (kt + 1 < ns) fetch(g, m0, n0);
-      __syncthreads();
-      compute(slot);
-    }
-  }
-  template <typename F>
-  __device__ __forceinline__ void for_each4(F f) const {
-    const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
-    const int row = wave / WN * (BM / WM) + (lane & 15);
-    const int col = wave % WN * (PWB / WN) + (lane >> 4) * 4;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      if constexpr (DUAL) {
-#pragma unroll
-        for (int j = 0; j < NIP; ++j)
-          f(row + i * 16, col + j * 16, acc[i][j], acc[i][NIP + j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-          f(row + i * 16, j / NIP * PWB + col + j % NIP * 16, acc[i][j], acc[i][j]);
-      }
+      for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r];
     }
   }
 };
@@ -457,7 +407,9 @@ __device__ __forceinline__ void tile_of(int id, int total, int tiles_m, int tile
   *tn = t / gm;
 }
 
-// The product with epilogue EP: ep(row, column, v0, v1) for 4 columns each; with
+// The product with epilogue EP: ep(row, column, v0, v1, pre) for W columns each (v1:
+// the second panel's values in a DUAL tile, else v0 again; pre: what EP::pre read
+// for them, one row block ahead so that the loads do not wait for each other); with
 // splits > 1 the sums go to g.part instead.
 template <typename Core, typename EP>
 __global__ __launch_bounds__(Core::THREADS) void gemm_kernel(GemmArgs g, EP ep) {
@@ -470,19 +422,40 @@ __global__ __launch_bounds__(Core::THREADS) void gemm_kernel(GemmArgs g, EP ep) 
   const int ns = g.stages - s0 < g.split_stages ? g.stages - s0 : g.split_stages;
   Core core;
   core.run(g, gemm_lds, m0, n0, s0, ns);
-  if (g.splits > 1) {
-    float* p0 = g.part + (int64_t)split * (Core::DUAL ? 2 : 1) * g.M * g.N;
-    core.for_each4([&](int r, int c, f32x4_t v0, f32x4_t v1) {
-      const int64_t m = m0 + r, n = n0 + c;
-      if (m >= g.M || n >= g.N) return;
-      store4(p0 + m * g.N + n, v0);
-      if constexpr (Core::DUAL) store4(p0 + (g.M + m) * g.N + n, v1);
-    });
-  } else {
-    core.for_each4([&](int r, int c, f32x4_t v0, f32x4_t v1) {
-      const int64_t m = m0 + r, n = n0 + c;
-      if (m < g.M && n < g.N) ep(m, n, v0, v1);
-    });
+  constexpr int W = Core::W, Q = Core::GROUPS;
+  using Pre = typename EP::template Pre<W>;
+  float* p0 = g.part + (int64_t)split * (Core::DUAL ? 2 : 1) * g.M * g.N;
+  const bool direct = g.splits == 1;
+  Pre pre[2][Q];
+  auto fetch = [&](int i) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int64_t m = m0 + core.group_row(i), n = n0 + core.group_col(q);
+      if (direct && m < g.M && n < g.N) ep.pre(m, n, pre[i & 1][q]);
+    }
+  };
+  fetch(0);
+#pragma unroll
+  for (int i = 0; i < Core::MI; ++i) {
+    if (i + 1 < Core::MI) fetch(i + 1);
+    __builtin_amdgcn_sched_barrier(0);  // one row block's values at a time
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int64_t m = m0 + core.group_row(i), n = n0 + core.group_col(q);
+      float v0[W], v1[W];
+      core.group_values(i, q, 0, v0);
+      if constexpr (Core::DUAL) core.group_values(i, q, 1, v1);
+      if (m >= g.M || n >= g.N) continue;
+      if (direct) {
+        if constexpr (Core::DUAL)
+          ep(m, n, v0, v1, pre[i & 1][q]);
+        else
+          ep(m, n, v0, v0, pre[i & 1][q]);
+      } else {
+        store_n(p0 + m * g.N + n, v0);
+        if constexpr (Core::DUAL) store_n(p0 + (g.M + m) * g.N + n, v1);
+      }
+    }
   }
 }
 
@@ -493,19 +466,26 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs g, EP ep) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < g.M * per;
        i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / per, n = i % per * 4;
-    f32x4_t v[2];
+    typename EP::template Pre<4> pre;
+    ep.pre(m, n, pre);
+    float v[2][4] = {};
 #pragma unroll
     for (int p = 0; p < (DUAL ? 2 : 1); ++p) {
       const float* q = g.part + ((int64_t)p * g.M + m) * g.N + n;
       const int64_t stride = (DUAL ? 2 : 1) * g.M * g.N;
-      v[p] = load4(q);
-      for (int s = 1; s < g.splits; ++s) {
-        const f32x4_t w = load4(q + s * stride);
+      // 8 splits' loads in flight; the sums are added in split order
+      for (int s = 0; s < g.splits; s += 8) {
+        f32x4_t w[8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[p][r] += w[r];
+        for (int e = 0; e < 8; ++e)
+          w[e] = s + e < g.splits ? load4(q + (s + e) * stride) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[p][r] += w[e][r];
       }
     }
-    ep(m, n, v[0], DUAL ? v[1] : v[0]);
+    ep(m, n, v[0], v[DUAL ? 1 : 0], pre);
   }
 }
 

@@ -7,22 +7,24 @@
 namespace moe {
 
 // A tile: rows x columns (of all panels), and what the choice goes by (from
-// measurement, in ns): one K stage of a workgroup that has a CU to itself, and
-// what a workgroup costs beyond its stages (first loads, epilogue).
+// measurement, in ns): one K stage of a workgroup that has a CU to itself, the
+// CU's time per stage when `per_cu` of them share it (as many as its LDS holds),
+// and what a workgroup costs beyond its stages (first loads, epilogue).
 struct TileCost {
   int bm, bn;
   int bk;
-  float stage_ns, fixed_ns;
+  int per_cu;
+  float alone_ns, busy_ns, fixed_ns;
 };
 constexpr TileCost kBfTiles[] = {
-    {256, 256, 64, 1100.f, 3000.f},
-    {128, 128, 64, 400.f, 2500.f},
-    {64, 128, 64, 260.f, 2500.f},
-    {16, 128, 64, 200.f, 2500.f},
+    {256, 256, 64, 1, 1550.f, 1550.f, 5000.f},
+    {128, 128, 64, 2, 620.f, 570.f, 4000.f},
+    {64, 128, 64, 2, 420.f, 390.f, 3500.f},
+    {16, 128, 64, 2, 400.f, 250.f, 3000.f},
 };
 constexpr TileCost kF32Tiles[] = {
-    {128, 128, 16, 1000.f, 2500.f},
-    {64, 64, 16, 300.f, 2000.f},
+    {128, 128, 32, 2, 2150.f, 2150.f, 2500.f},
+    {64, 64, 32, 5, 850.f, 570.f, 2000.f},
 };
 constexpr int kCus = 256;
 
@@ -33,8 +35,9 @@ struct GemmPlan {
   size_t part_bytes;
 };
 
-// The tile and the splits with the least estimated time: rounds of workgroups
-// over the CUs times a workgroup's time, plus the splits' sums' way through memory.
+// The tile and the splits with the least estimated time: the workgroups of a CU, as
+// many at once as it holds, plus the splits' sums' way through memory and the
+// launch that joins them.
 // `tiles`: bit mask of the tiles that the product has kernels for.
 inline GemmPlan plan_gemm(bool f32, unsigned tiles, bool dual, int64_t M, int64_t N, int64_t K,
                           int pairs) {
@@ -56,12 +59,19 @@ inline GemmPlan plan_gemm(bool f32, unsigned tiles, bool dual, int64_t M, int64_
       p.splits = (p.stages + p.split_stages - 1) / p.split_stages;
       if (p.splits != s) continue;
       if (s > 1 && wgs * s > 4 * kCus) break;
-      const float rounds = (float)((wgs * s + kCus - 1) / kCus);
-      float ns = rounds * (c.fixed_ns + p.split_stages * c.stage_ns);
+      const int64_t per = (wgs * s + kCus - 1) / kCus;  // workgroups of the fullest CU
+      float ns = 0.f;
+      for (int64_t left = per; left > 0; left -= c.per_cu) {
+        const float at_once = (float)(left < c.per_cu ? left : c.per_cu);
+        const float stage =
+            c.alone_ns > at_once * c.busy_ns ? c.alone_ns : at_once * c.busy_ns;
+        ns += c.fixed_ns + p.split_stages * stage;
+        if (ns > best_ns) break;
+      }
       p.part_bytes = 0;
       if (s > 1) {
         p.part_bytes = (size_t)s * (dual ? 2 : 1) * (size_t)M * (size_t)N * 4;
-        ns += 3000.f + (float)p.part_bytes * 2.f / 4000.f;
+        ns += 5000.f + (float)p.part_bytes * 2.f / 5000.f;
       }
       if (ns < best_ns) {
         best_ns = ns;
@@ -100,57 +110,64 @@ constexpr unsigned tile_mask(bool f32) {
 
 template <typename T, bool DUAL, bool AKC, bool BKC, typename EP>
 void launch_gemm(const GemmPlan& p, const GemmArgs& g, const EP& ep, hipStream_t st) {
+  constexpr int NP = DUAL ? 2 : 1;
   if constexpr (sizeof(T) == 4) {
     if (p.tile == 0)
-      launch_tile<F32Core<128, 128, 2, DUAL, AKC, BKC>>(g, ep, st);
+      launch_tile<TileCore<T, 128, 128, 2, DUAL, AKC, BKC, 2, 4, 2>>(g, ep, st);
     else
-      launch_tile<F32Core<64, 64, 2, DUAL, AKC, BKC>>(g, ep, st);
+      launch_tile<TileCore<T, 64, 64, NP, DUAL, AKC, BKC, 2, 2, 2>>(g, ep, st);
   } else {
-    constexpr int NP = DUAL ? 2 : 1;
     if (p.tile == 0)
-      launch_tile<BfCore<256, 256, 2, DUAL, AKC, BKC, 2, 4, 2>>(g, ep, st);
+      launch_tile<TileCore<T, 256, 256, 2, DUAL, AKC, BKC, 2, 4, 2>>(g, ep, st);
     else if (p.tile == 1)
-      launch_tile<BfCore<128, 128, NP, DUAL, AKC, BKC, 2, 4, 4>>(g, ep, st);
+      launch_tile<TileCore<T, 128, 128, NP, DUAL, AKC, BKC, 2, 4, 2>>(g, ep, st);
     else if (p.tile == 2)
-      launch_tile<BfCore<64, 128, NP, DUAL, AKC, BKC, 2, 4, 6>>(g, ep, st);
+      launch_tile<TileCore<T, 64, 128, NP, DUAL, AKC, BKC, 2, 4, 3>>(g, ep, st);
     else if constexpr (AKC)
-      launch_tile<BfCore<16, 128, NP, DUAL, AKC, BKC, 1, 4, 8>>(g, ep, st);
+      launch_tile<TileCore<T, 16, 128, NP, DUAL, AKC, BKC, 1, 4, 4>>(g, ep, st);
   }
 }
 
 // ------------------------------------------------------------ epilogues
+struct NoPre {};
+
 // h = SiLU(u) g from the fp32 sums; u and g kept for a backward pass.
 template <typename T>
 struct EpSwiglu {
   T *h, *U, *G;
   int64_t ld;
-  __device__ __forceinline__ void operator()(int64_t m, int64_t n, f32x4_t u, f32x4_t g) const {
+  template <int W>
+  using Pre = NoPre;
+  template <typename P>
+  __device__ __forceinline__ void pre(int64_t, int64_t, P&) const {}
+  template <int W, typename P>
+  __device__ __forceinline__ void operator()(int64_t m, int64_t n, const float (&u)[W],
+                                             const float (&g)[W], const P&) const {
     const int64_t o = m * ld + n;
-    f32x4_t v;
+    float v[W];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = silu_f32(u[r]) * g[r];
-    store4(h + o, v);
+    for (int r = 0; r < W; ++r) v[r] = silu_f32(u[r]) * g[r];
+    store_n(h + o, v);
     if (U != nullptr) {
-      store4(U + o, u);
-      store4(G + o, g);
+      store_n(U + o, u);
+      store_n(G + o, g);
     }
   }
 };
-template <typename T>
+// One output, or the two panels' (DUAL).
+template <typename T, bool DUAL = false>
 struct EpStore {
-  T* out;
-  int64_t ld;
-  __device__ __forceinline__ void operator()(int64_t m, int64_t n, f32x4_t v, f32x4_t) const {
-    store4(out + m * ld + n, v);
-  }
-};
-template <typename T>
-struct EpStore2 {
   T *out0, *out1;
   int64_t ld;
-  __device__ __forceinline__ void operator()(int64_t m, int64_t n, f32x4_t v0, f32x4_t v1) const {
-    store4(out0 + m * ld + n, v0);
-    store4(out1 + m * ld + n, v1);
+  template <int W>
+  using Pre = NoPre;
+  template <typename P>
+  __device__ __forceinline__ void pre(int64_t, int64_t, P&) const {}
+  template <int W, typename P>
+  __device__ __forceinline__ void operator()(int64_t m, int64_t n, const float (&v0)[W],
+                                             const float (&v1)[W], const P&) const {
+    store_n(out0 + m * ld + n, v0);
+    if constexpr (DUAL) store_n(out1 + m * ld + n, v1);
   }
 };
 // From dh: dU, dG, and h again (all operands of the products that follow); h may
@@ -160,21 +177,32 @@ struct EpSwigluBwd {
   const T *U, *G;
   T *dU, *dG, *h;
   int64_t ld;
-  __device__ __forceinline__ void operator()(int64_t m, int64_t n, f32x4_t dh, f32x4_t) const {
+  template <int W>
+  struct Pre {
+    Pack<T, W> u, g;
+  };
+  template <int W>
+  __device__ __forceinline__ void pre(int64_t m, int64_t n, Pre<W>& p) const {
+    p.u.load(U + m * ld + n);
+    p.g.load(G + m * ld + n);
+  }
+  template <int W>
+  __device__ __forceinline__ void operator()(int64_t m, int64_t n, const float (&dh)[W],
+                                             const float (&)[W], const Pre<W>& p) const {
     const int64_t o = m * ld + n;
-    const f32x4_t u = load4(U + o), g = load4(G + o);
-    f32x4_t du, dg, hv;
+    float du[W], dg[W], hv[W];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-u[r]));
-      const float a = u[r] * s;
+    for (int r = 0; r < W; ++r) {
+      const float u = p.u.get(r), g = p.g.get(r);
+      const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+      const float a = u * s;
       dg[r] = dh[r] * a;
-      du[r] = dh[r] * g[r] * (s * (1.0f + u[r] * (1.0f - s)));
-      hv[r] = a * g[r];
+      du[r] = dh[r] * g * (s * (1.0f + u * (1.0f - s)));
+      hv[r] = a * g;
     }
-    store4(dU + o, du);
-    store4(dG + o, dg);
-    if (h != nullptr) store4(h + o, hv);
+    store_n(dU + o, du);
+    store_n(dG + o, dg);
+    if (h != nullptr) store_n(h + o, hv);
   }
 };
 

@@ -329,7 +329,7 @@ __global__ void w4_combine_kernel(int64_t S, int64_t H, int k, int E, const int3
   const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
   if (i >= S * H) return;
   const int64_t t = i / H, c = i % H;
-  f32x4_t a = {0.f, 0.f, 0.f, 0.f};
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
   for (int j = 0; j < k; ++j) {
     const int id = ids[t * k + j];
     if (id < 0 || id >= E) continue;
@@ -343,7 +343,7 @@ __global__ void w4_combine_kernel(int64_t S, int64_t H, int k, int E, const int3
 #pragma unroll
     for (int r = 0; r < 4; ++r) a[r] += v[r];
   }
-  store4(O + i, a);
+  store_n(O + i, a);
 }
 
 moe_status enqueued() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }

@@ -11,6 +11,8 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from . import (MOE_BF16, MOE_F32, MOE_OUTPUT_F32, _check, _stream, _ws, load_library, moe_shape)
 
 __all__ = ["moe_ffn_shape", "make_ffn_shape", "moe_layernorm_forward",
@@ -65,12 +67,13 @@ def bind(lib) -> None:
 
 
 def _types(dtype):
-    import torch
     return {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}.get(dtype)
 
 
 class _Args:
     """The tensors of one call: checks each, keeps their common device."""
+
+    __slots__ = ("call", "device")
 
     def __init__(self, call):
         self.call = call
@@ -78,42 +81,58 @@ class _Args:
 
     def __call__(self, name, t, shape=None, dtype=None, optional=False):
         """Address of a contiguous device tensor (None for an absent optional one)."""
-        import torch
+        if t is None and optional:
+            return None
+        # one test for the usual case (decode calls take a few microseconds in all)
+        if (type(t) is torch.Tensor and t.is_cuda and (dtype is None or t.dtype == dtype)
+                and (shape is None or t.shape == shape) and t.is_contiguous()):
+            d = t.get_device()
+            if d == self.device or self.device is None:
+                self.device = d
+                return t.data_ptr() or None
+        return self.refuse(name, t, shape, dtype)
+
+    def refuse(self, name, t, shape, dtype):
         if t is None:
-            if optional:
-                return None
             raise TypeError(f"{self.call}: {name} is required")
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{self.call}: {name} must be a tensor, not {type(t).__name__}")
         if t.device.type != "cuda":
             raise ValueError(f"{self.call}: {name} is on {t.device}: the library takes device "
                              "memory")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{self.call}: {name} is on {t.device}, others on {self.device}")
+        if self.device is not None and t.get_device() != self.device:
+            raise ValueError(f"{self.call}: {name} is on {t.device}, others on "
+                             f"cuda:{self.device}")
         if dtype is not None and t.dtype != dtype:
             raise ValueError(f"{self.call}: {name} is {t.dtype}, not {dtype}")
         if shape is not None and tuple(t.shape) != tuple(shape):
             raise ValueError(f"{self.call}: {name} is {tuple(t.shape)}, not {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{self.call}: {name} must be contiguous")
-        return t.data_ptr() if t.numel() else None
+        self.device = t.get_device()  # a subclass of Tensor
+        return t.data_ptr() or None
 
     def workspace(self, ws):
         if isinstance(ws, tuple):
             return _ws(ws)
-        return self("workspace", ws, optional=True), 0 if ws is None else \
-            ws.numel() * ws.element_size()
+        return self("workspace", ws, optional=True), 0 if ws is None else ws.nbytes
 
     def run(self, stream, check, *args):
         """The call on the tensors' device, its status checked."""
-        import torch
-        with torch.cuda.device(self.device):
-            code = getattr(load_library(), self.call)(*args, _stream(stream))
-        if check:
+        d = self.device
+        f = getattr(load_library(), self.call)
+        if d == torch.cuda.current_device():
+            code = f(*args, _raw_stream(d) if stream is None else _stream(stream))
+        else:
+            with torch.cuda.device(d):
+                code = f(*args, _raw_stream(d) if stream is None else _stream(stream))
+        if check and code:
             _check(self.call, code)
         return code
+
+
+def _raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _matrix(call, name, t):
@@ -123,7 +142,6 @@ def _matrix(call, name, t):
 
 
 def _float_dtype(call, name, t):
-    import torch
     if t.dtype == torch.float32:
         return MOE_F32
     if t.dtype == torch.bfloat16:
@@ -137,7 +155,6 @@ def moe_layernorm_forward(X, gamma, beta, eps, Y, mean=None, rstd=None, stream=N
                           check=True) -> int:
     """Y = layer norm of the rows of X [S][H]; gamma and beta [H] or None; mean
     and rstd [S] float32, kept for the backward pass, or None."""
-    import torch
     a = _Args("moe_layernorm_forward")
     S, H = _matrix(a.call, "X", X)
     dt = _float_dtype(a.call, "X", X)
@@ -156,7 +173,6 @@ def moe_layernorm_backward_workspace_bytes(S: int, H: int, dtype: int = MOE_BF16
 def moe_layernorm_backward(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, workspace, stream=None,
                            check=True) -> int:
     """dX [S][H], and dgamma and dbeta [H] float32 (or None for both)."""
-    import torch
     a = _Args("moe_layernorm_backward")
     S, H = _matrix(a.call, "X", X)
     dt = _float_dtype(a.call, "X", X)
@@ -180,7 +196,6 @@ def moe_ffn_forward(shape, X, W_up, W_gate, W_down, U, G, O, workspace, stream=N
                     check=True) -> int:
     """O = (SiLU(X W_up) * (X W_gate)) W_down; U and G (the pre-activations) are
     kept for moe_ffn_backward, or None."""
-    import torch
     a = _Args("moe_ffn_forward")
     S, H, D, t = shape.S, shape.H, shape.D, _types(shape.dtype)
     to = torch.float32 if shape.flags & MOE_OUTPUT_F32 else t
@@ -200,7 +215,6 @@ def moe_ffn_backward(shape, dO, X, W_up, W_gate, W_down, U, G, dX, dW_up, dW_gat
                      workspace, stream=None, check=True) -> int:
     """Gradients from dO and the kept U and G. dX may be None; the weight
     gradients may be None together."""
-    import torch
     a = _Args("moe_ffn_backward")
     S, H, D, t = shape.S, shape.H, shape.D, _types(shape.dtype)
     tw = torch.float32 if shape.flags & MOE_OUTPUT_F32 else t
@@ -236,7 +250,6 @@ def _w4_shapes(call, codes, group):
 def moe_quantize_w4(W, group, codes, scales, stream=None, check=True) -> int:
     """Codes (uint8, W's shape) and scales (bfloat16, [.., ceil(K / group), N])
     of a bfloat16 or float32 tensor W [E][K][N] or [K][N]."""
-    import torch
     a = _Args("moe_quantize_w4")
     E, K, N = _ekn(a.call, "W", W)
     dt = _float_dtype(a.call, "W", W)
@@ -248,7 +261,6 @@ def moe_quantize_w4(W, group, codes, scales, stream=None, check=True) -> int:
 def moe_pack_w4_weights(codes, scales, group, packed, stream=None, check=True) -> int:
     """Codes and scales laid out for the products, into ``packed``
     (moe_w4_weight_bytes(E, K, N, group) bytes, uint8)."""
-    import torch
     a = _Args("moe_pack_w4_weights")
     E, K, N, ss = _w4_shapes(a.call, codes, group)
     need = moe_w4_weight_bytes(E, K, N, group)
@@ -261,14 +273,13 @@ def moe_w4_matvec(X, W, Y, expert_ids=None, stream=None, check=True) -> int:
     """Y = X W for few rows X [S][K] (bfloat16) and a packed weight W
     (layer.W4Weight); Y [S][N] bfloat16 or float32; expert_ids [S] int32: the
     matrix each row takes (none: row of zeros)."""
-    import torch
     a = _Args("moe_w4_matvec")
     S, K = _matrix(a.call, "X", X)
     if K != W.K:
         raise ValueError(f"moe_w4_matvec: X has {K} columns, W {W.K} rows")
     flags = MOE_OUTPUT_F32 if _float_dtype(a.call, "Y", Y) == MOE_F32 else 0
     return a.run(stream, check, S, K, W.N, W.E, W.group, flags, a("X", X, None, torch.bfloat16),
-                 a("W", W.packed, (moe_w4_weight_bytes(W.E, W.K, W.N, W.group),), torch.uint8),
+                 a("W", W.packed, (W.nbytes,), torch.uint8),
                  a("expert_ids", expert_ids, (S,), torch.int32, optional=True),
                  a("Y", Y, (S, W.N)))
 
@@ -282,7 +293,6 @@ def moe_w4_forward(shape, A, W_up, W_gate, W_down, Ws_up, Ws_gate, Ws_down, topk
     """The MoE layer's experts with 4-bit weights (layer.W4Weight each, the shared
     expert's None without one) on few tokens, from the router's topk_ids and
     topk_weights."""
-    import torch
     a = _Args("moe_w4_forward")
     S, H, D, Ds, E, k = (shape.S, shape.H, shape.D, shape.D_shared, shape.E, shape.k)
     group = W_up.group
@@ -292,7 +302,7 @@ def moe_w4_forward(shape, A, W_up, W_gate, W_down, Ws_up, Ws_gate, Ws_down, topk
             return None
         if (w.E, w.K, w.N, w.group) != want + (group,):
             raise ValueError(f"{a.call}: {name} is {w}, not {want} in groups of {group}")
-        return a(name, w.packed, (moe_w4_weight_bytes(*want, group),), torch.uint8)
+        return a(name, w.packed, (w.nbytes,), torch.uint8)
 
     to = torch.float32 if shape.flags & MOE_OUTPUT_F32 else torch.bfloat16
     args = [ctypes.byref(shape), group, a("A", A, (S, H), torch.bfloat16),

@@ -161,8 +161,8 @@ class W4Weight:
     def __init__(self, codes, scales, group=128, stream=None):
         self.E, self.K, self.N = (1, *codes.shape) if codes.dim() == 2 else tuple(codes.shape)
         self.group = group
-        self.packed = torch.empty(moe_w4_weight_bytes(self.E, self.K, self.N, group),
-                                  dtype=torch.uint8, device=codes.device)
+        self.nbytes = moe_w4_weight_bytes(self.E, self.K, self.N, group)
+        self.packed = torch.empty(self.nbytes, dtype=torch.uint8, device=codes.device)
         moe_pack_w4_weights(codes, scales, group, self.packed, stream)
 
     @classmethod
