@@ -11,15 +11,35 @@
 // workspace, [workgroups][2][H], and a second kernel adds them in a fixed
 // order: no atomics, the same bits on every run.
 //
-// A row is shared by TPR threads: a wave where its registers hold the row, else
-// the workgroup. Rows too long for that are read again for each sum (they
-// then come from L2).
+// A row is shared by TPR threads: a wave where its registers hold the row (no
+// barrier then), else a workgroup of 256 or 512. Rows too long for that are read
+// again for each sum (they then come from L2). The workgroups walk over the rows,
+// a few to a CU, and the next row's loads are out before the sums of the current
+// one: what gamma, beta (and their gradients' sums) hold stays in registers.
 #include "ffn_common.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the kernels that share rows by waves, or re-read them
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xF, 0xF,
+                                                         false));
+}
+// Sum over a wave in every lane, without LDS: exchanges within quads, half rows and
+// rows of 16 lanes, then between rows and halves.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0xB1>(v);   // quad_perm 1 0 3 2
+  v = dpp_add<0x4E>(v);   // quad_perm 2 3 0 1
+  v = dpp_add<0x141>(v);  // row_half_mirror
+  v = dpp_add<0x140>(v);  // row_mirror
+  auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+  w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(w[0]) + __uint_as_float(w[1]);
+}
 
 // Sum over the TPR threads of a row: a wave's by lane exchange, a workgroup's
 // through LDS in wave order. `red` has room for 2 x (waves) x NV floats and is
@@ -27,9 +47,7 @@ constexpr int kThreads = 256;
 template <int TPR, int NV>
 __device__ __forceinline__ void row_sum(float (&v)[NV], float* red, int& par) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v[i] += __shfl_xor(v[i], o);
+  for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     float* r = red + par * W * NV;
@@ -47,86 +65,118 @@ __device__ __forceinline__ void row_sum(float (&v)[NV], float* red, int& par) {
   }
 }
 
-// VEC consecutive elements of p as floats (VEC = 1, or 16 bytes of them).
+// VEC consecutive elements as loaded (one of them, or 16 bytes). Rows are read and
+// written once: vectors both with the non-temporal hint (16384 x 7168 bf16, cold
+// caches: forward 119 -> 88 us, backward 169 -> 131 us, 5.4 TB/s; the hint on the
+// stores alone made them slower). Not single elements, whose accesses share cache
+// lines with each other's (4099 x 1001 fp32 backward out of a warm cache: 18 us
+// with the hint, 15 us without).
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&f)[VEC]) {
-  if constexpr (VEC == 1) {
-    f[0] = to_f32<T>(p[0]);
-  } else {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const Vec16<T> t = __builtin_bit_cast(Vec16<T>, w);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = to_f32<T>(t.v[i]);
+struct Raw {
+  T v[VEC];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC == 1)
+      v[0] = p[0];
+    else
+      *this = __builtin_bit_cast(Raw, *reinterpret_cast<const f32x4_t*>(p));
   }
-}
+  __device__ __forceinline__ void load_once(const T* p) {
+    if constexpr (VEC == 1)
+      v[0] = p[0];
+    else
+      *this = __builtin_bit_cast(
+          Raw, __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p)));
+  }
+  __device__ __forceinline__ float operator[](int i) const { return to_f32<T>(v[i]); }
+};
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T* p, const float (&f)[VEC]) {
-  if constexpr (VEC == 1) {
-    p[0] = from_f32<T>(f[0]);
-  } else {
-    Vec16<T> t;
+  Raw<T, VEC> t;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) t.v[i] = from_f32<T>(f[i]);
-    *reinterpret_cast<uint4*>(p) = __builtin_bit_cast(uint4, t);
+  for (int i = 0; i < VEC; ++i) t.v[i] = from_f32<T>(f[i]);
+  if constexpr (VEC == 1)
+    p[0] = t.v[0];
+  else
+    __builtin_nontemporal_store(__builtin_bit_cast(f32x4_t, t), reinterpret_cast<f32x4_t*>(p));
+}
+
+// Column sums: 4 to a store (whole 16-byte vectors wherever rows are).
+template <int VEC>
+__device__ __forceinline__ void store_sums(float* p, const float (&f)[VEC]) {
+  if constexpr (VEC == 1)
+    p[0] = f[0];
+  else
+    store_n(p, f);
+}
+
+// This thread's vectors of a row (IT of them, TPR apart).
+template <typename T, int VEC, int TPR, int IT, bool ONCE = true>
+__device__ __forceinline__ void load_row(const T* row, int64_t H, int t, Raw<T, VEC> (&v)[IT]) {
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int c = (i * TPR + t) * VEC;
+    if (c < H) {
+      if constexpr (ONCE)
+        v[i].load_once(row + c);
+      else
+        v[i].load(row + c);
+    }
   }
 }
 
+template <int TPR>
+constexpr int group_threads() { return TPR > kThreads ? TPR : kThreads; }
+
 // Rows of at most TPR * VEC * IT elements, held in registers.
 template <typename T, int VEC, int TPR, int IT>
-__global__ __launch_bounds__(kThreads) void ln_fwd_kernel(int64_t S, int64_t H, const T* X,
-                                                          const T* gamma, const T* beta,
-                                                          float eps, T* Y, float* mean,
-                                                          float* rstd) {
-  constexpr int RPB = kThreads / TPR;
+__global__ __launch_bounds__(group_threads<TPR>()) void ln_fwd_kernel(
+    int64_t S, int64_t H, const T* X, const T* gamma, const T* beta, float eps, T* Y, float* mean,
+    float* rstd) {
+  constexpr int RPB = group_threads<TPR>() / TPR;
   __shared__ float red[2 * (TPR / 64)];
   int par = 0;
   const int t = threadIdx.x % TPR;
+  const int64_t stride = (int64_t)gridDim.x * RPB;
   // the same rows for every thread of a row's TPR: barriers stay uniform
-  for (int64_t s = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; s < S;
-       s += (int64_t)gridDim.x * RPB) {
-    const T* x = X + s * H;
+  int64_t s = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  Raw<T, VEC> g[IT], b[IT], next[IT];
+  if (gamma) load_row<T, VEC, TPR, IT, false>(gamma, H, t, g);
+  if (beta) load_row<T, VEC, TPR, IT, false>(beta, H, t, b);
+  if (s < S) load_row<T, VEC, TPR, IT>(X + s * H, H, t, next);
+  for (; s < S; s += stride) {
     float v[IT][VEC];
-    float sum[1] = {0.f};
-  #pragma unroll
+    float sum[1] = {0.f}, sq[1] = {0.f};
+#pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int64_t c = ((int64_t)i * TPR + t) * VEC;
-      if (c < H) {
-        load_vec<T, VEC>(x + c, v[i]);
-      } else {
-  #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
+      const bool in = (i * TPR + t) * VEC < H;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        v[i][e] = in ? next[i][e] : 0.f;
+        sum[0] += v[i][e];
       }
     }
-  #pragma unroll
-    for (int i = 0; i < IT; ++i)
-  #pragma unroll
-      for (int e = 0; e < VEC; ++e) sum[0] += v[i][e];
+    if (s + stride < S) load_row<T, VEC, TPR, IT>(X + (s + stride) * H, H, t, next);
     row_sum<TPR, 1>(sum, red, par);
     const float m = sum[0] / (float)H;
-    float sq[1] = {0.f};
-  #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int64_t c = ((int64_t)i * TPR + t) * VEC;
-      if (c < H)
-  #pragma unroll
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+      if ((i * TPR + t) * VEC < H)
+#pragma unroll
         for (int e = 0; e < VEC; ++e) {
           v[i][e] -= m;
           sq[0] += v[i][e] * v[i][e];
         }
-    }
     row_sum<TPR, 1>(sq, red, par);
     const float r = 1.0f / sqrtf(sq[0] / (float)H + eps);
     T* y = Y + s * H;
-  #pragma unroll
+#pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int64_t c = ((int64_t)i * TPR + t) * VEC;
+      const int c = (i * TPR + t) * VEC;
       if (c < H) {
-        float g[VEC], b[VEC], o[VEC];
-        if (gamma) load_vec<T, VEC>(gamma + c, g);
-        if (beta) load_vec<T, VEC>(beta + c, b);
-  #pragma unroll
+        float o[VEC];
+#pragma unroll
         for (int e = 0; e < VEC; ++e)
-          o[e] = v[i][e] * r * (gamma ? g[e] : 1.f) + (beta ? b[e] : 0.f);
+          o[e] = v[i][e] * r * (gamma ? g[i][e] : 1.f) + (beta ? b[i][e] : 0.f);
         store_vec<T, VEC>(y + c, o);
       }
     }
@@ -149,30 +199,31 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_long_kernel(int64_t S, int64_
     const T* x = X + s * H;
     float sum[1] = {0.f}, sq[1] = {0.f};
     for (int64_t c = (int64_t)threadIdx.x * VEC; c < H; c += kThreads * VEC) {
-      float v[VEC];
-      load_vec<T, VEC>(x + c, v);
-  #pragma unroll
+      Raw<T, VEC> v;
+      v.load(x + c);
+#pragma unroll
       for (int e = 0; e < VEC; ++e) sum[0] += v[e];
     }
     row_sum<kThreads, 1>(sum, red, par);
     const float m = sum[0] / (float)H;
     for (int64_t c = (int64_t)threadIdx.x * VEC; c < H; c += kThreads * VEC) {
-      float v[VEC];
-      load_vec<T, VEC>(x + c, v);
-  #pragma unroll
+      Raw<T, VEC> v;
+      v.load(x + c);
+#pragma unroll
       for (int e = 0; e < VEC; ++e) sq[0] += (v[e] - m) * (v[e] - m);
     }
     row_sum<kThreads, 1>(sq, red, par);
     const float r = 1.0f / sqrtf(sq[0] / (float)H + eps);
     for (int64_t c = (int64_t)threadIdx.x * VEC; c < H; c += kThreads * VEC) {
-      float v[VEC], g[VEC], b[VEC];
-      load_vec<T, VEC>(x + c, v);
-      if (gamma) load_vec<T, VEC>(gamma + c, g);
-      if (beta) load_vec<T, VEC>(beta + c, b);
-  #pragma unroll
+      Raw<T, VEC> v, g, b;
+      v.load(x + c);
+      if (gamma) g.load(gamma + c);
+      if (beta) b.load(beta + c);
+      float o[VEC];
+#pragma unroll
       for (int e = 0; e < VEC; ++e)
-        v[e] = (v[e] - m) * r * (gamma ? g[e] : 1.f) + (beta ? b[e] : 0.f);
-      store_vec<T, VEC>(Y + s * H + c, v);
+        o[e] = (v[e] - m) * r * (gamma ? g[e] : 1.f) + (beta ? b[e] : 0.f);
+      store_vec<T, VEC>(Y + s * H + c, o);
     }
     if (mean != nullptr && threadIdx.x == 0) {
       mean[s] = m;
@@ -184,58 +235,59 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_long_kernel(int64_t S, int64_
 // Backward for rows held in registers. part: [gridDim.x][2][H] (dgamma, dbeta
 // of this workgroup's rows), or null.
 template <typename T, int VEC, int TPR, int IT>
-__global__ __launch_bounds__(kThreads) void ln_bwd_kernel(int64_t S, int64_t H, const T* dY,
-                                                          const T* X, const T* gamma,
-                                                          const float* mean, const float* rstd,
-                                                          T* dX, float* part) {
-  constexpr int RPB = kThreads / TPR;
+__global__ __launch_bounds__(group_threads<TPR>()) void ln_bwd_kernel(
+    int64_t S, int64_t H, const T* dY, const T* X, const T* gamma, const float* mean,
+    const float* rstd, T* dX, float* part) {
+  constexpr int RPB = group_threads<TPR>() / TPR;
   __shared__ float red[2 * 2 * (TPR / 64)];
   int par = 0;
   const int t = threadIdx.x % TPR;
   const int sub = threadIdx.x / TPR;
-  float g[IT][VEC], ag[IT][VEC], ab[IT][VEC];
+  Raw<T, VEC> g[IT], nx[IT], nd[IT];
+  float ag[IT][VEC], ab[IT][VEC];
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int64_t c = ((int64_t)i * TPR + t) * VEC;
+  for (int i = 0; i < IT; ++i)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      g[i][e] = 1.f;
-      ag[i][e] = ab[i][e] = 0.f;
-    }
-    if (gamma && c < H) load_vec<T, VEC>(gamma + c, g[i]);
-  }
+    for (int e = 0; e < VEC; ++e) ag[i][e] = ab[i][e] = 0.f;
+  if (gamma) load_row<T, VEC, TPR, IT, false>(gamma, H, t, g);
   const float inv = 1.0f / (float)H;
-  for (int64_t s = (int64_t)blockIdx.x * RPB + sub; s < S; s += (int64_t)gridDim.x * RPB) {
-    const float m = mean[s], r = rstd[s];
+  const int64_t stride = (int64_t)gridDim.x * RPB;
+  int64_t s = (int64_t)blockIdx.x * RPB + sub;
+  float nm = 0.f, nr = 0.f;
+  if (s < S) {
+    load_row<T, VEC, TPR, IT>(X + s * H, H, t, nx);
+    load_row<T, VEC, TPR, IT>(dY + s * H, H, t, nd);
+    nm = mean[s];
+    nr = rstd[s];
+  }
+  for (; s < S; s += stride) {
+    const float m = nm, r = nr;
     float n[IT][VEC], d[IT][VEC];
     float sums[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int64_t c = ((int64_t)i * TPR + t) * VEC;
-      if (c < H) {
-        load_vec<T, VEC>(X + s * H + c, n[i]);
-        load_vec<T, VEC>(dY + s * H + c, d[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int64_t c = ((int64_t)i * TPR + t) * VEC;
-      if (c < H)
+    for (int i = 0; i < IT; ++i)
+      if ((i * TPR + t) * VEC < H)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          n[i][e] = (n[i][e] - m) * r;
+          n[i][e] = (nx[i][e] - m) * r;
+          d[i][e] = nd[i][e];
           ag[i][e] += d[i][e] * n[i][e];
           ab[i][e] += d[i][e];
-          d[i][e] *= g[i][e];
+          if (gamma) d[i][e] *= g[i][e];
           sums[0] += d[i][e];
           sums[1] += d[i][e] * n[i][e];
         }
+    if (s + stride < S) {
+      load_row<T, VEC, TPR, IT>(X + (s + stride) * H, H, t, nx);
+      load_row<T, VEC, TPR, IT>(dY + (s + stride) * H, H, t, nd);
+      nm = mean[s + stride];
+      nr = rstd[s + stride];
     }
     row_sum<TPR, 2>(sums, red, par);
     const float c0 = sums[0] * inv, c1 = sums[1] * inv;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int64_t c = ((int64_t)i * TPR + t) * VEC;
+      const int c = (i * TPR + t) * VEC;
       if (c < H) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) d[i][e] = r * (d[i][e] - c0 - n[i][e] * c1);
@@ -249,12 +301,10 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(int64_t S, int64_t H, 
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const int64_t c = ((int64_t)i * TPR + t) * VEC;
-      if (c < H)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          pg[c + e] = ag[i][e];
-          pg[H + c + e] = ab[i][e];
-        }
+      if (c < H) {
+        store_sums<VEC>(pg + c, ag[i]);
+        store_sums<VEC>(pg + H + c, ab[i]);
+      }
     }
   } else {
     // the waves' columns added in wave order through LDS
@@ -284,8 +334,9 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(int64_t S, int64_t H, 
 
 // dX of rows of any length (two passes over the row).
 template <typename T, int VEC>
-__global__ __launch_bounds__(kThreads) void ln_bwd_long_kernel(int64_t S, int64_t H, const T* dY, const T* X,
-                                                               const T* gamma, const float* mean,
+__global__ __launch_bounds__(kThreads) void ln_bwd_long_kernel(int64_t S, int64_t H, const T* dY,
+                                                               const T* X, const T* gamma,
+                                                               const float* mean,
                                                                const float* rstd, T* dX) {
   __shared__ float red[2 * 2 * (kThreads / 64)];
   int par = 0;
@@ -293,11 +344,11 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_long_kernel(int64_t S, int64_
     const float m = mean[s], r = rstd[s];
     float sums[2] = {0.f, 0.f};
     for (int64_t c = (int64_t)threadIdx.x * VEC; c < H; c += kThreads * VEC) {
-      float x[VEC], d[VEC], g[VEC];
-      load_vec<T, VEC>(X + s * H + c, x);
-      load_vec<T, VEC>(dY + s * H + c, d);
-      if (gamma) load_vec<T, VEC>(gamma + c, g);
-  #pragma unroll
+      Raw<T, VEC> x, d, g;
+      x.load(X + s * H + c);
+      d.load(dY + s * H + c);
+      if (gamma) g.load(gamma + c);
+#pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float dg = gamma ? d[e] * g[e] : d[e];
         sums[0] += dg;
@@ -308,16 +359,17 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_long_kernel(int64_t S, int64_
     const float inv = 1.0f / (float)H;
     const float c0 = sums[0] * inv, c1 = sums[1] * inv;
     for (int64_t c = (int64_t)threadIdx.x * VEC; c < H; c += kThreads * VEC) {
-      float x[VEC], d[VEC], g[VEC];
-      load_vec<T, VEC>(X + s * H + c, x);
-      load_vec<T, VEC>(dY + s * H + c, d);
-      if (gamma) load_vec<T, VEC>(gamma + c, g);
-  #pragma unroll
+      Raw<T, VEC> x, d, g;
+      x.load(X + s * H + c);
+      d.load(dY + s * H + c);
+      if (gamma) g.load(gamma + c);
+      float o[VEC];
+#pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float dg = gamma ? d[e] * g[e] : d[e];
-        d[e] = r * (dg - c0 - (x[e] - m) * r * c1);
+        o[e] = r * (dg - c0 - (x[e] - m) * r * c1);
       }
-      store_vec<T, VEC>(dX + s * H + c, d);
+      store_vec<T, VEC>(dX + s * H + c, o);
     }
   }
 }
@@ -340,29 +392,39 @@ __global__ __launch_bounds__(kThreads) void ln_cols_kernel(int64_t S, int64_t H,
   part[(int64_t)blockIdx.y * 2 * H + H + c] = b;
 }
 
-// dgamma, dbeta: the P partial sums of each of 2 H columns in a fixed order,
-// 64 columns per workgroup, each wave a quarter of the partials.
-__global__ __launch_bounds__(kThreads) void ln_reduce_kernel(int64_t P, int64_t H,
-                                                             const float* part, float* dgamma,
-                                                             float* dbeta) {
-  __shared__ float red[kThreads / 64][64];
+// dgamma, dbeta: the P partial sums of each of 2 H columns in a fixed order: 64
+// columns per workgroup, each of 16 waves a sixteenth of the partials, 8 loads at
+// a time. (4 waves with one load at a time took 60 us for P = 512, H = 2048: one
+// memory latency after another.)
+__global__ __launch_bounds__(1024) void ln_reduce_kernel(int64_t P, int64_t H, const float* part,
+                                                         float* dgamma, float* dbeta) {
+  constexpr int W = 16, B = 8;
+  __shared__ float red[W][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t j = (int64_t)blockIdx.x * 64 + lane;
   float a = 0.f;
   if (j < 2 * H)
-    for (int64_t p = w; p < P; p += kThreads / 64) a += part[p * 2 * H + j];
+    for (int64_t p = w; p < P; p += W * B) {
+      float v[B];
+#pragma unroll
+      for (int e = 0; e < B; ++e) v[e] = p + e * W < P ? part[(p + e * W) * 2 * H + j] : 0.f;
+#pragma unroll
+      for (int e = 0; e < B; ++e) a += v[e];
+    }
   red[w][lane] = a;
   __syncthreads();
   if (w == 0 && j < 2 * H) {
 #pragma unroll
-    for (int q = 1; q < kThreads / 64; ++q) a += red[q][lane];
+    for (int q = 1; q < W; ++q) a += red[q][lane];
     (j < H ? dgamma[j] : dbeta[j - H]) = a;
   }
 }
 
-// Which kernel takes a row: a wave per row up to 4 vectors (or 8 elements) per
-// lane, a workgroup per row up to 8 vectors (16 elements) per thread, else the
-// re-reading kernels.
+// Which kernel takes a row: a wave per row up to 1 vector (or 4 elements) per lane,
+// a workgroup of 256 or 512 per row up to 4 vectors (16 elements) per thread, else
+// the re-reading kernels. (Rows of 4 vectors per lane by waves: 66 us where a
+// workgroup per row takes 58, 16384 x 2048 bf16 backward: too few rows in flight
+// at 220 registers.)
 struct LnPlan {
   bool vec;
   int tpr, it;  // it = 0: long rows
@@ -371,51 +433,59 @@ LnPlan ln_plan(int64_t H, int es, bool aligned) {
   LnPlan p;
   p.vec = aligned && (H * es) % 16 == 0;
   const int64_t v = p.vec ? 16 / es : 1;
-  const int wave_it = p.vec ? 4 : 8, wg_it = p.vec ? 8 : 16;
-  auto pow2 = [](int64_t n) {
-    int r = 1;
-    while (r < n) r *= 2;
-    return r;
-  };
-  if (H <= 64 * v * wave_it) {
-    p.tpr = 64;
-    p.it = pow2((H + 64 * v - 1) / (64 * v));
-  } else if (H <= kThreads * v * wg_it) {
-    p.tpr = kThreads;
-    p.it = pow2((H + kThreads * v - 1) / (kThreads * v));
-  } else {
-    p.tpr = kThreads;
-    p.it = 0;
+  for (int tpr : {64, 256, 512}) {
+    const int64_t it = (H + tpr * v - 1) / (tpr * v);
+    if (it > (p.vec ? (tpr == 64 ? 1 : 4) : (tpr == 64 ? 4 : 16))) continue;
+    p.tpr = tpr;
+    p.it = (int)it;
+    if (!p.vec)  // compiled for 1, 2, 4, 8 and 16
+      for (p.it = 1; p.it < it; p.it *= 2) {
+      }
+    return p;
   }
+  p.tpr = kThreads;
+  p.it = 0;
   return p;
 }
 
-constexpr int64_t kBwdGroups = 512;  // most workgroups of the backward pass (partial sums each)
+// Most workgroups of the backward pass, each with partial sums of its own (1024: dX
+// as fast, the sums' way through memory twice as long).
+constexpr int64_t kBwdGroups = 512;
+constexpr int64_t kRowGroups = 2048;  // of the forward pass: 8 of 256 threads to a CU
 
 int64_t bwd_groups(int64_t S, const LnPlan& p) {
-  const int64_t rpb = kThreads / p.tpr;
+  const int64_t rpb = p.tpr < kThreads ? kThreads / p.tpr : 1;
   const int64_t n = (S + rpb - 1) / rpb;
   return n < kBwdGroups ? n : kBwdGroups;
 }
 
 template <typename T, int VEC, typename F>
-bool dispatch(const LnPlan& p, F f) {
-#define MOE_LN_CASE(TPR, IT)                                              \
-  if (p.tpr == TPR && p.it == IT) {                                       \
-    f(std::integral_constant<int, TPR>{}, std::integral_constant<int, IT>{}); \
-    return true;                                                          \
-  }
-  MOE_LN_CASE(64, 1) MOE_LN_CASE(64, 2) MOE_LN_CASE(64, 4)
-  if constexpr (VEC == 1) { MOE_LN_CASE(64, 8) }
-  MOE_LN_CASE(256, 1) MOE_LN_CASE(256, 2) MOE_LN_CASE(256, 4) MOE_LN_CASE(256, 8)
-  if constexpr (VEC == 1) { MOE_LN_CASE(256, 16) }
-#undef MOE_LN_CASE
-  return false;
+void dispatch(const LnPlan& p, F f) {
+  auto with = [&](auto tpr) {
+    auto it = [&](auto n) {
+      if (p.tpr == decltype(tpr)::value && p.it == decltype(n)::value) f(tpr, n);
+    };
+    it(std::integral_constant<int, 1>{});
+    if constexpr (VEC == 1 || decltype(tpr)::value > 64) {
+      it(std::integral_constant<int, 2>{});
+      it(std::integral_constant<int, 4>{});
+    }
+    if constexpr (decltype(tpr)::value > 64) {
+      if constexpr (VEC > 1) {
+        it(std::integral_constant<int, 3>{});
+      } else {
+        it(std::integral_constant<int, 8>{});
+        it(std::integral_constant<int, 16>{});
+      }
+    }
+  };
+  with(std::integral_constant<int, 64>{});
+  with(std::integral_constant<int, 256>{});
+  with(std::integral_constant<int, 512>{});
 }
 
-// Workgroups over n rows (a launch holds fewer than 2^32 threads; the kernels
-// walk over further rows).
-unsigned row_grid(int64_t n) { return (unsigned)(n < (1 << 20) ? n : (1 << 20)); }
+// Workgroups over n rows; the kernels walk over further rows.
+unsigned row_grid(int64_t n) { return (unsigned)(n < kRowGroups ? n : kRowGroups); }
 
 template <typename T, int VEC>
 void forward_t(const LnPlan& p, int64_t S, int64_t H, const T* X, const T* gamma, const T* beta,
@@ -426,10 +496,9 @@ void forward_t(const LnPlan& p, int64_t S, int64_t H, const T* X, const T* gamma
     return;
   }
   dispatch<T, VEC>(p, [&](auto tpr, auto it) {
-    constexpr int RPB = kThreads / decltype(tpr)::value;
-    ln_fwd_kernel<T, VEC, decltype(tpr)::value, decltype(it)::value>
-        <<<row_grid((S + RPB - 1) / RPB), kThreads, 0, st>>>(S, H, X, gamma, beta, eps, Y,
-                                                               mean, rstd);
+    constexpr int TPR = decltype(tpr)::value, NT = group_threads<TPR>(), RPB = NT / TPR;
+    ln_fwd_kernel<T, VEC, TPR, decltype(it)::value>
+        <<<row_grid((S + RPB - 1) / RPB), NT, 0, st>>>(S, H, X, gamma, beta, eps, Y, mean, rstd);
   });
 }
 
@@ -446,8 +515,10 @@ void backward_t(const LnPlan& p, int64_t S, int64_t H, const T* dY, const T* X, 
     return;
   }
   dispatch<T, VEC>(p, [&](auto tpr, auto it) {
-    ln_bwd_kernel<T, VEC, decltype(tpr)::value, decltype(it)::value>
-        <<<(unsigned)groups, kThreads, 0, st>>>(S, H, dY, X, gamma, mean, rstd, dX, part);
+    constexpr int TPR = decltype(tpr)::value;
+    ln_bwd_kernel<T, VEC, TPR, decltype(it)::value>
+        <<<(unsigned)groups, group_threads<TPR>(), 0, st>>>(S, H, dY, X, gamma, mean, rstd, dX,
+                                                            part);
   });
 }
 
@@ -555,7 +626,7 @@ extern "C" moe_status moe_layernorm_backward(int64_t S, int64_t H, int32_t dtype
       go(bf16_t{});
   }
   if (dgamma != nullptr)
-    ln_reduce_kernel<<<(unsigned)((2 * H + 63) / 64), kThreads, 0, (hipStream_t)stream>>>(
+    ln_reduce_kernel<<<(unsigned)((2 * H + 63) / 64), 1024, 0, (hipStream_t)stream>>>(
         S > 0 ? groups : 0, H, part, dgamma, dbeta);
   return enqueued();
 }
