@@ -125,7 +125,7 @@ moe_status moe_ffn_backward(const moe_ffn_shape* shape, const void* dO, const vo
  * 1024 bytes of codes: 16 bytes for each lane l = 16 q + c (column c), dword i
  * of which holds the 8 rows 32 i + 8 q + j, row j in bits 4 (j / 2) + 16 (j % 2)
  * to + 3, the whole dword then rotated left by 3 bits; then its scales
- * [128 / group][16] bf16. Both calls are one-time steps, at weight load. K and
+ * [16][128 / group] bf16. Both calls are one-time steps, at weight load. K and
  * N multiples of 8, below 2^22.
  */
 size_t moe_w4_weight_bytes(int64_t E, int64_t K, int64_t N, int32_t group); /* 0 if unsupported */
@@ -137,7 +137,7 @@ moe_status moe_pack_w4_weights(const uint8_t* codes, const void* scales, int64_t
 /*
  * Y = X W for few rows (decode): X [S][K] bf16, W packed with E matrices, Y
  * [S][N] bf16, or fp32 with flags = MOE_OUTPUT_F32. The weights are read once
- * per 16 rows; made for S up to a few tens, S <= 4096.
+ * per 16 rows; made for S up to a few tens, S <= 4096 and X below 2 GiB.
  *   expert_ids  [S] int32 or NULL. NULL: every row takes matrix 0. Else row s
  *               takes matrix expert_ids[s] (rows may share one, and its weights
  *               are then read once for 16 of them); an id outside [0, E) gives
@@ -160,7 +160,8 @@ moe_status moe_w4_matvec(int64_t S, int64_t K, int64_t N, int64_t E, int32_t gro
  * whose slots are all empty (padding) and no shared expert gives a row of
  * zeros. An expert's weights are read once per 16 of its rows.
  *   shape     dtype MOE_BF16, capacity 0, flags 0 or MOE_OUTPUT_F32, S * k and S at
- *             most 4096; block_size and renormalize are not looked at
+ *             most 4096, A and the h rows below 2 GiB; block_size and renormalize
+ *             are not looked at
  *   A         [S][H] bf16;  W_up, W_gate: packed [E][H][D];  W_down: packed [E][D][H];
  *   Ws_*      packed with E = 1 ([H][D_shared] twice, [D_shared][H]), NULL iff D_shared = 0
  *   O         [S][H] bf16, or fp32 with MOE_OUTPUT_F32

@@ -48,7 +48,7 @@ def test_packed_layout(E, K, N, group):
             for k in range(kt):
                 at = ((e * nt + ct) * kt + k) * tb
                 words = p[at:at + 1024].view(torch.int32).view(64, 4)
-                sc = p[at + 1024:at + tb].view(torch.int16).view(-1, 16)
+                sc = p[at + 1024:at + tb].view(torch.int16).view(16, -1)
                 for lane in range(0, 64, 5):
                     n, q = ct * 16 + lane % 16, lane // 16
                     for i in range(4):
@@ -59,10 +59,10 @@ def test_packed_layout(E, K, N, group):
                             v |= code << (4 * (j // 2) + 16 * (j % 2))
                         v = ((v << 3) | (v >> 29)) & 0xFFFFFFFF
                         assert int(words[lane, i]) & 0xFFFFFFFF == v
-                    for gi in range(sc.shape[0]):
+                    for gi in range(sc.shape[1]):
                         gg = k * (128 // group) + gi
                         want = int(s[e, gg, n]) if gg < s.shape[1] and n < N else 0
-                        assert int(sc[gi, lane % 16]) == want
+                        assert int(sc[lane % 16, gi]) == want
 
 
 SIZES = [(1, 8, 8), (1, 128, 16), (1, 2048, 1000), (2, 136, 24), (3, 2056, 264), (15, 200, 72),
