@@ -121,18 +121,20 @@ class _Args:
         """The call on the tensors' device, its status checked."""
         d = self.device
         f = getattr(load_library(), self.call)
+        st = _raw_stream(d) if stream is None else _stream(stream)
         if d == torch.cuda.current_device():
-            code = f(*args, _raw_stream(d) if stream is None else _stream(stream))
+            code = f(*args, st)
         else:
             with torch.cuda.device(d):
-                code = f(*args, _raw_stream(d) if stream is None else _stream(stream))
+                code = f(*args, st)
         if check and code:
             _check(self.call, code)
         return code
 
 
-def _raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+# the current stream's handle of a device, without a Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _matrix(call, name, t):
