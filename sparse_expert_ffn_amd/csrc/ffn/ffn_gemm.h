@@ -62,7 +62,7 @@ __device__ __forceinline__ i32x4_t window_srd(uint64_t base, int64_t left) {
 // KC: row r at r * 128 bytes, its 16-byte chunk c in slot c ^ (r / 2) % 8.
 // MC: panel by panel, K row k of a panel at k * ROWB bytes; its units (32 bytes in
 // bf16, 64 in fp32: 16 columns) u in slot u ^ swz_mc(k).
-template <typename T, bool KC, int R, int PW, int BASES, int NW>
+template <typename T, bool KC, int R, int PW, int BASES, int NW, bool ONCE>
 struct Operand {
   static constexpr int ES = sizeof(T);
   static constexpr int BK = 128 / ES;          // K values per stage
@@ -164,7 +164,7 @@ struct Operand {
     const i32x4_t r = b == 0 ? srd[0] : srd[BASES - 1];
     uint32_t o = off[t];
     if constexpr (KC) o = chunk_k < kleft ? o : kOutOfRange;
-    dma16(r, o, lds + q * 1024);
+    dma16<false, ONCE>(r, o, lds + q * 1024);
   }
   // Fragment of the wave's 16-row (column) block j of panel p for K step ks. MC: a
   // wave's blocks lie in one panel and start at a multiple of their number, so
@@ -193,8 +193,11 @@ struct Operand {
 // BM x BN tile by WM x WN waves, NP column panels of BN / NP, DUAL: each panel
 // has a B and a C of its own. A wave covers the same BN / NP / WN columns of each
 // panel. NST: LDS slots.
+// ONCE: B is read once in all (one row of tiles): its loads carry the non-temporal hint
+// (64 tokens of 7168 x 2048, cold caches: up and gate 28.6 -> 16.8 us, down 15.7 ->
+// 13.1 us; one token 25.8 -> 14.3 and 14.5 -> 8.9 us).
 template <typename T, int BM_, int BN_, int NP_, bool DUAL_, bool AKC, bool BKC, int WM, int WN,
-          int NST_>
+          int NST_, bool ONCE = false>
 struct TileCore {
   static constexpr int BM = BM_, BN = BN_, NP = NP_, BK = 128 / (int)sizeof(T), NST = NST_;
   static constexpr bool DUAL = DUAL_;
@@ -202,71 +205,80 @@ struct TileCore {
   static constexpr int PWB = BN / NP;
   static constexpr int PMAX = 256 / (int)sizeof(T);
   static constexpr int PWA = AKC ? BM : (BM < PMAX ? BM : PMAX);
-  using OpA = Operand<T, AKC, BM, PWA, 1, NW>;
-  using OpB = Operand<T, BKC, BN, PWB, DUAL ? 2 : 1, NW>;
+  using OpA = Operand<T, AKC, BM, PWA, 1, NW, false>;
+  using OpB = Operand<T, BKC, BN, PWB, DUAL ? 2 : 1, NW, ONCE>;
   static constexpr int MI = BM / WM / 16;
   static constexpr int NIP = PWB / WN / 16;  // 16-column blocks per wave and panel
   static constexpr int NI = NP * NIP;
   static constexpr int STAGE = OpA::BYTES + OpB::BYTES;
-  static constexpr int LDS_BYTES = NST * STAGE;
   // loads every wave issues per stage, at least
   static constexpr int MIN_PW = OpA::INSTR / NW + OpB::INSTR / NW;
   static constexpr int PIECES = OpA::PER_WAVE + OpB::PER_WAVE;
   static_assert(MI >= 1 && NIP >= 1, "tile too small for the waves");
   static_assert(AKC || (PWA % (BM / WM) == 0 && (MI & (MI - 1)) == 0), "A blocks in one panel");
   static_assert(BKC || (NIP & (NIP - 1)) == 0, "B blocks");
-  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
   static_assert((NST - 1) * PIECES < 64, "vmcnt range");
 
   f32x4_t acc[MI][NI];
   OpA a;
   OpB b;
-  int kleft;      // K values of the current pair from the next stage to issue on
-  int pair;
+  // Where an operand's next stage to load lies: its pair, the pair's K values from
+  // that stage on, the stages still to load.
+  struct Cursor {
+    int pair, kleft, stages;
+  };
+  Cursor ca, cb;
 
-  __device__ __forceinline__ void seek(const GemmArgs& g, int64_t m0, int64_t n0, int64_t k0) {
-    a.seek(0, g.A[pair], g.lda, m0, g.M, g.K[pair], k0);
-    b.seek(0, g.B[pair][0], g.ldb, n0, g.N, g.K[pair], k0);
-    if constexpr (DUAL) b.seek(1, g.B[pair][1], g.ldb, n0, g.N, g.K[pair], k0);
-    kleft = (int)(g.K[pair] - k0);
+  __device__ __forceinline__ void seek_a(const GemmArgs& g, int64_t m0, int64_t k0) {
+    a.seek(0, g.A[ca.pair], g.lda, m0, g.M, g.K[ca.pair], k0);
+    ca.kleft = (int)(g.K[ca.pair] - k0);
   }
-  __device__ __forceinline__ void issue_piece(char* slot, int i) const {
-    if (i < OpA::PER_WAVE)
-      a.issue(slot, i, kleft);
-    else
-      b.issue(slot + OpA::BYTES, i - OpA::PER_WAVE, kleft);
+  __device__ __forceinline__ void seek_b(const GemmArgs& g, int64_t n0, int64_t k0) {
+    b.seek(0, g.B[cb.pair][0], g.ldb, n0, g.N, g.K[cb.pair], k0);
+    if constexpr (DUAL) b.seek(1, g.B[cb.pair][1], g.ldb, n0, g.N, g.K[cb.pair], k0);
+    cb.kleft = (int)(g.K[cb.pair] - k0);
   }
-  // To the next stage to issue (past the last one: loads give zeros).
-  __device__ __forceinline__ void next_stage(const GemmArgs& g, int64_t m0, int64_t n0) {
-    kleft -= BK;
-    if (kleft <= 0 && pair + 1 < g.pairs) {
-      ++pair;
-      seek(g, m0, n0, 0);
+  // To the next stage to load; past the last one loads give zeros.
+  template <typename Op, typename Seek>
+  __device__ __forceinline__ static void next(Op& op, Cursor& c, int pairs, Seek seek) {
+    c.kleft -= BK;
+    if (--c.stages <= 0) {
+      c.kleft = 0;
+      op.close();
+    } else if (c.kleft <= 0 && c.pair + 1 < pairs) {
+      ++c.pair;
+      seek();
     } else {
-      a.advance();
-      b.advance();
+      op.advance();
     }
   }
+  __device__ __forceinline__ void next_a(const GemmArgs& g, int64_t m0) {
+    next(a, ca, g.pairs, [&] { seek_a(g, m0, 0); });
+  }
+  __device__ __forceinline__ void next_b(const GemmArgs& g, int64_t n0) {
+    next(b, cb, g.pairs, [&] { seek_b(g, n0, 0); });
+  }
 
-  uint4 fa[2][MI], fb[2][NI];  // fragments of two K steps of 32 in turn
+  uint4 fa[2][MI], fb[2][NI];  // fragments of two K steps in turn
 
   // Fragment n of K step ks (B's column blocks, then A's row blocks) into set `to`.
-  __device__ __forceinline__ void read_frag(const char* slot, int ks, int to, int n) {
+  __device__ __forceinline__ void read_frag(const char* la, const char* lb, int ks, int to,
+                                            int n) {
     if (n < NI)
-      fb[to][n] = b.frag(slot + OpA::BYTES, n / NIP, n % NIP, ks);
+      fb[to][n] = b.frag(lb, n / NIP, n % NIP, ks);
     else
-      fa[to][n - NI] = a.frag(slot, 0, n - NI, ks);
+      fa[to][n - NI] = a.frag(la, 0, n - NI, ks);
   }
 
   // The MFMAs of the K step in set `cur`, row block by row block; between them go
-  // the LDS reads of the next K step (from rd, into the other set; all of them out
-  // two row blocks before the end, so that they have landed when it starts) and,
-  // with `issue`, the global loads of a later stage into wr.
-  __device__ __forceinline__ void phase(int cur, const char* rd, int rd_ks, char* wr,
-                                        bool issue) {
+  // the LDS reads of the next K step (from la and lb, into the other set; all of them
+  // out a row block before the end, so that they have landed when it starts) and
+  // `loads` global loads of a later stage, issue(n), over the first `rows` row blocks.
+  template <typename Issue>
+  __device__ __forceinline__ void phase(int cur, const char* la, const char* lb, int ks, int loads,
+                                        int rows, Issue issue) {
     constexpr int FRAGS = NI + MI;
     constexpr int ROWS = MI > 2 ? MI - 1 : MI;  // row blocks that carry reads
-    constexpr int IROWS = MI < 4 ? MI : 4;      // and global loads
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
 #pragma unroll
@@ -285,21 +297,32 @@ struct TileCore {
       if (i < ROWS) {
 #pragma unroll
         for (int n = i * FRAGS / ROWS; n < (i + 1) * FRAGS / ROWS; ++n)
-          read_frag(rd, rd_ks, cur ^ 1, n);
+          read_frag(la, lb, ks, cur ^ 1, n);
       }
-      if (issue)
 #pragma unroll
-        for (int n = i * PIECES / IROWS; n < (i + 1) * PIECES / IROWS && n < PIECES; ++n)
-          issue_piece(wr, n);
+      for (int n = i * loads / rows; n < (i + 1) * loads / rows && n < loads; ++n) issue(n);
       __builtin_amdgcn_sched_barrier(0);  // the order of the row blocks stands
     }
   }
 
-  // K stages [s0, s0 + ns) of the tile at (m0, n0). All NST slots are in flight.
+  // K stages [s0, s0 + ns) of the tile at (m0, n0).
+  //
   // Stage kt: its first K step's fragments were read during the previous phase;
-  // phase 0 reads the second K step's; then every wave's reads of the slot are done
-  // and stage kt + 1 has landed (one wait and barrier), and phase 1 reads stage
-  // kt + 1's first fragments and loads stage kt + NST into stage kt's slot.
+  // phase 0 reads the second K step's; then every wave's reads of the stage's LDS are
+  // done and stage kt + 1 has landed (one wait and barrier), and phase 1 reads stage
+  // kt + 1's first fragments.
+  //
+  // Whole slots: all NST are in flight, phase 1 loads stage kt + NST into stage kt's.
+  // HALVES (the 256 x 256 tile, whose LDS holds two stages and a half): A and B have
+  // slots of their own, five in turn (A0 B0 A1 B1 A2 B2 ..), phase 0 loads A of stage
+  // kt + 2 into the one that B of kt - 1 left and phase 1 B of stage kt + 2 into that of
+  // A of kt: half the loads in each phase instead of all of them in one.
+  static constexpr bool HALVES = OpA::BYTES == OpB::BYTES && 5 * OpA::BYTES <= 160 * 1024 &&
+                                 6 * OpA::BYTES > 160 * 1024;
+  static constexpr int LDS_BYTES = HALVES ? 5 * OpA::BYTES : NST * STAGE;
+  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+  static_assert(!HALVES || (OpA::INSTR % NW == 0 && OpB::INSTR % NW == 0), "even loads");
+
   __device__ __forceinline__ void run(const GemmArgs& g, char* lds, int64_t m0, int64_t n0,
                                       int s0, int ns) {
 #pragma unroll
@@ -310,39 +333,92 @@ struct TileCore {
     a.setup(wave, g.lda, m0, g.M, wave / WN * (BM / WM));
     b.setup(wave, g.ldb, n0, g.N, wave % WN * (PWB / WN));
     const int first = (int)((g.K[0] + BK - 1) / BK);  // stages of pair 0
-    pair = s0 < first ? 0 : 1;
-    seek(g, m0, n0, (int64_t)(s0 - (pair ? first : 0)) * BK);
-    int to_issue = ns;
-    auto finish = [&] {
-      next_stage(g, m0, n0);
-      if (--to_issue <= 0) {  // stages past the last one load nothing (zeros)
-        kleft = 0;
-        pair = 2;
-        a.close();
-        b.close();
+    ca.pair = cb.pair = s0 < first ? 0 : 1;
+    ca.stages = cb.stages = ns;
+    const int64_t k0 = (int64_t)(s0 - (ca.pair ? first : 0)) * BK;
+    seek_a(g, m0, k0);
+    seek_b(g, n0, k0);
+    auto load_a = [&](char* to, int n) { a.issue(to, n, ca.kleft); };
+    auto load_b = [&](char* to, int n) { b.issue(to, n, cb.kleft); };
+    constexpr int PA = OpA::PER_WAVE, PB = OpB::PER_WAVE;
+    if constexpr (HALVES) {
+      constexpr int H = OpA::BYTES;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int n = 0; n < PA; ++n) load_a(lds + 2 * s * H, n);
+        next_a(g, m0);
+#pragma unroll
+        for (int n = 0; n < PB; ++n) load_b(lds + (2 * s + 1) * H, n);
+        next_b(g, n0);
       }
-    };
-#pragma unroll
-    for (int s = 0; s < NST; ++s) {
-#pragma unroll
-      for (int i = 0; i < PIECES; ++i) issue_piece(lds + s * STAGE, i);
-      finish();
-    }
-    wait_vmcnt<(NST - 1) * MIN_PW>();
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NI + MI; ++n) read_frag(lds, 0, 0, n);
-    int slot = 0;
-    for (int kt = 0; kt < ns; ++kt) {
-      char* cur = lds + slot * STAGE;
-      slot = slot + 1 == NST ? 0 : slot + 1;
-      phase(0, cur, 1, nullptr, false);
-      wait_vmcnt<(NST - 2) * MIN_PW>();
+      wait_vmcnt<PA + PB>();
       __syncthreads();
-      __builtin_amdgcn_sched_barrier(0);
-      phase(1, lds + slot * STAGE, 0, cur, true);
-      finish();
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < NI + MI; ++n) read_frag(lds, lds + H, 0, 0, n);
+      int u = 0;  // slot of A of stage kt
+      auto at = [&](int d) { return lds + (u + d >= 5 ? u + d - 5 : u + d) * H; };
+      for (int kt = 0; kt < ns; ++kt) {
+        char* to_a = at(4);
+        phase(0, at(0), at(1), 1, PA, 4, [&](int n) { load_a(to_a, n); });
+        next_a(g, m0);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<PA>();
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        char* to_b = at(0);
+        phase(1, at(2), at(3), 0, PB, 4, [&](int n) { load_b(to_b, n); });
+        next_b(g, n0);
+        u = u + 2 >= 5 ? u - 3 : u + 2;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      // both operands go through K together: one cursor
+      auto load = [&](char* to, int n) {
+        if (n < PA)
+          a.issue(to, n, ca.kleft);
+        else
+          b.issue(to + OpA::BYTES, n - PA, ca.kleft);
+      };
+      auto next_ab = [&] {
+        ca.kleft -= BK;
+        if (--ca.stages <= 0) {
+          ca.kleft = 0;
+          a.close();
+          b.close();
+        } else if (ca.kleft <= 0 && ca.pair + 1 < g.pairs) {
+          cb.pair = ++ca.pair;
+          seek_a(g, m0, 0);
+          seek_b(g, n0, 0);
+        } else {
+          a.advance();
+          b.advance();
+        }
+      };
+#pragma unroll
+      for (int s = 0; s < NST; ++s) {
+#pragma unroll
+        for (int n = 0; n < PA + PB; ++n) load(lds + s * STAGE, n);
+        next_ab();
+      }
+      wait_vmcnt<(NST - 1) * MIN_PW>();
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NI + MI; ++n) read_frag(lds, lds + OpA::BYTES, 0, 0, n);
+      int slot = 0;
+      for (int kt = 0; kt < ns; ++kt) {
+        char* cur = lds + slot * STAGE;
+        slot = slot + 1 == NST ? 0 : slot + 1;
+        const char* nxt = lds + slot * STAGE;
+        phase(0, cur, cur + OpA::BYTES, 1, 0, 1, [](int) {});
+        wait_vmcnt<(NST - 2) * MIN_PW>();
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        phase(1, nxt, nxt + OpA::BYTES, 0, PA + PB, MI < 4 ? MI : 4,
+              [&](int n) { load(cur, n); });
+        next_ab();
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     wait_vmcnt<0>();
   }
@@ -468,22 +544,25 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs g, EP ep) {
     const int64_t m = i / per, n = i % per * 4;
     typename EP::template Pre<4> pre;
     ep.pre(m, n, pre);
+    constexpr int P = DUAL ? 2 : 1;
     float v[2][4] = {};
+    const float* q = g.part + m * g.N + n;
+    const int64_t panel = g.M * g.N;
+    // 8 splits' loads in flight; the sums are added in split order
+    for (int s = 0; s < g.splits; s += 8) {
+      f32x4_t w[8][P];
 #pragma unroll
-    for (int p = 0; p < (DUAL ? 2 : 1); ++p) {
-      const float* q = g.part + ((int64_t)p * g.M + m) * g.N + n;
-      const int64_t stride = (DUAL ? 2 : 1) * g.M * g.N;
-      // 8 splits' loads in flight; the sums are added in split order
-      for (int s = 0; s < g.splits; s += 8) {
-        f32x4_t w[8];
+      for (int e = 0; e < 8; ++e)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          w[e] = s + e < g.splits ? load4(q + (s + e) * stride) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < P; ++p)
+          w[e][p] = s + e < g.splits ? load4(q + ((s + e) * P + p) * panel)
+                                     : f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < 8; ++e)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[p][r] += w[e][r];
-      }
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[p][r] += w[e][p][r];
     }
     ep(m, n, v[0], v[DUAL ? 1 : 0], pre);
   }

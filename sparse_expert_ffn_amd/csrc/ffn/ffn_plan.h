@@ -17,10 +17,11 @@ struct TileCost {
   float alone_ns, busy_ns, fixed_ns;
 };
 constexpr TileCost kBfTiles[] = {
-    {256, 256, 64, 1, 1550.f, 1550.f, 5000.f},
-    {128, 128, 64, 2, 620.f, 570.f, 4000.f},
+    {256, 256, 64, 1, 1560.f, 1560.f, 6000.f},
+    {128, 128, 64, 2, 720.f, 570.f, 4000.f},
     {64, 128, 64, 2, 420.f, 390.f, 3500.f},
     {16, 128, 64, 2, 400.f, 250.f, 3000.f},
+    {256, 128, 64, 1, 950.f, 950.f, 4500.f},
 };
 constexpr TileCost kF32Tiles[] = {
     {128, 128, 32, 2, 2150.f, 2150.f, 2500.f},
@@ -43,7 +44,7 @@ inline GemmPlan plan_gemm(bool f32, unsigned tiles, bool dual, int64_t M, int64_
                           int pairs) {
   GemmPlan best = {};
   float best_ns = 3.0e38f;
-  const int n = f32 ? 2 : 4;
+  const int n = f32 ? 2 : 5;
   for (int t = 0; t < n; ++t) {
     if (!(tiles >> t & 1)) continue;
     const TileCost& c = f32 ? kF32Tiles[t] : kBfTiles[t];
@@ -71,7 +72,7 @@ inline GemmPlan plan_gemm(bool f32, unsigned tiles, bool dual, int64_t M, int64_
       p.part_bytes = 0;
       if (s > 1) {
         p.part_bytes = (size_t)s * (dual ? 2 : 1) * (size_t)M * (size_t)N * 4;
-        ns += 5000.f + (float)p.part_bytes * 2.f / 5000.f;
+        ns += 5000.f + (float)p.part_bytes * 2.f / 9000.f;
       }
       if (ns < best_ns) {
         best_ns = ns;
@@ -105,7 +106,7 @@ void launch_tile(const GemmArgs& g, const EP& ep, hipStream_t st) {
 // The tiles of a product with these operand orders.
 template <bool DUAL, bool AKC, bool BKC>
 constexpr unsigned tile_mask(bool f32) {
-  return f32 ? 3u : AKC ? 15u : 7u;  // 16 rows: K-contiguous A only
+  return f32 ? 3u : AKC ? 31u : 23u;  // 16 rows: K-contiguous A only
 }
 
 template <typename T, bool DUAL, bool AKC, bool BKC, typename EP>
@@ -121,10 +122,18 @@ void launch_gemm(const GemmPlan& p, const GemmArgs& g, const EP& ep, hipStream_t
       launch_tile<TileCore<T, 256, 256, 2, DUAL, AKC, BKC, 2, 4, 2>>(g, ep, st);
     else if (p.tile == 1)
       launch_tile<TileCore<T, 128, 128, NP, DUAL, AKC, BKC, 2, 4, 2>>(g, ep, st);
+    else if (p.tile == 4)
+      launch_tile<TileCore<T, 256, 128, NP, DUAL, AKC, BKC, 4, 2, 3>>(g, ep, st);
+    else if (p.tile == 2 && p.tiles_m == 1)
+      launch_tile<TileCore<T, 64, 128, NP, DUAL, AKC, BKC, 2, 4, 3, true>>(g, ep, st);
     else if (p.tile == 2)
       launch_tile<TileCore<T, 64, 128, NP, DUAL, AKC, BKC, 2, 4, 3>>(g, ep, st);
-    else if constexpr (AKC)
-      launch_tile<TileCore<T, 16, 128, NP, DUAL, AKC, BKC, 1, 4, 4>>(g, ep, st);
+    else if constexpr (AKC) {
+      if (p.tiles_m == 1)
+        launch_tile<TileCore<T, 16, 128, NP, DUAL, AKC, BKC, 1, 4, 4, true>>(g, ep, st);
+      else
+        launch_tile<TileCore<T, 16, 128, NP, DUAL, AKC, BKC, 1, 4, 4>>(g, ep, st);
+    }
   }
 }
 
