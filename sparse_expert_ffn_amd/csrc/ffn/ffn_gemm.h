@@ -278,7 +278,7 @@ struct TileCore {
   __device__ __forceinline__ void phase(int cur, const char* la, const char* lb, int ks, int loads,
                                         int rows, Issue issue) {
     constexpr int FRAGS = NI + MI;
-    constexpr int ROWS = MI > 2 ? MI - 1 : MI;  // row blocks that carry reads
+    constexpr int ROWS = MI > 1 ? MI - 1 : 1;   // row blocks that carry reads
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
 #pragma unroll

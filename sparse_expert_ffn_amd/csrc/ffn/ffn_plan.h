@@ -6,26 +6,24 @@
 
 namespace moe {
 
-// A tile: rows x columns (of all panels), and what the choice goes by (from
-// measurement, in ns): one K stage of a workgroup that has a CU to itself, the
-// CU's time per stage when `per_cu` of them share it (as many as its LDS holds),
-// and what a workgroup costs beyond its stages (first loads, epilogue).
+// A tile: rows x columns (of all panels), K per stage, workgroups that a CU's LDS
+// holds, and its times in ns, fitted to measured products (16384 x 2048 x 4096 down to
+// 64 x 2048 x 768): a CU that runs n of them takes wait + n busy for a K stage of each;
+// fixed is what a workgroup takes beyond its stages (launch, first loads, epilogue).
 struct TileCost {
-  int bm, bn;
-  int bk;
-  int per_cu;
-  float alone_ns, busy_ns, fixed_ns;
+  int bm, bn, bk, per_cu;
+  float wait_ns, busy_ns, fixed_ns;
 };
 constexpr TileCost kBfTiles[] = {
-    {256, 256, 64, 1, 1560.f, 1560.f, 6000.f},
-    {128, 128, 64, 2, 720.f, 570.f, 4000.f},
-    {64, 128, 64, 2, 420.f, 390.f, 3500.f},
-    {16, 128, 64, 2, 400.f, 250.f, 3000.f},
-    {256, 128, 64, 1, 950.f, 950.f, 4500.f},
+    {256, 256, 64, 1, 0.f, 1560.f, 6000.f},
+    {128, 128, 64, 2, 280.f, 440.f, 4000.f},
+    {64, 128, 64, 2, 50.f, 370.f, 3500.f},
+    {16, 128, 64, 2, 150.f, 250.f, 3000.f},
+    {256, 128, 64, 1, 0.f, 950.f, 4500.f},
 };
 constexpr TileCost kF32Tiles[] = {
-    {128, 128, 32, 2, 2150.f, 2150.f, 2500.f},
-    {64, 64, 32, 5, 850.f, 570.f, 2000.f},
+    {128, 128, 32, 2, 70.f, 2130.f, 2500.f},
+    {64, 64, 32, 5, 300.f, 510.f, 2000.f},
 };
 constexpr int kCus = 256;
 
@@ -64,9 +62,7 @@ inline GemmPlan plan_gemm(bool f32, unsigned tiles, bool dual, int64_t M, int64_
       float ns = 0.f;
       for (int64_t left = per; left > 0; left -= c.per_cu) {
         const float at_once = (float)(left < c.per_cu ? left : c.per_cu);
-        const float stage =
-            c.alone_ns > at_once * c.busy_ns ? c.alone_ns : at_once * c.busy_ns;
-        ns += c.fixed_ns + p.split_stages * stage;
+        ns += c.fixed_ns + p.split_stages * (c.wait_ns + at_once * c.busy_ns);
         if (ns > best_ns) break;
       }
       p.part_bytes = 0;
