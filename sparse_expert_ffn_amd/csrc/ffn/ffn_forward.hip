@@ -74,7 +74,7 @@ moe_status check_ffn(const moe_ffn_shape* s) {
   if (s->dtype == MOE_MXFP8 || s->H % 8 || s->D % 8 || s->H >= (1 << 22) || s->D >= (1 << 22) ||
       s->S >= INT32_MAX - 256)
     return MOE_ERR_UNSUPPORTED;
-  // a launch's workgroups (of at most 512 threads, below 2^32 in all), for any tile
+  // a launch's workgroups, in tiles of 64 x 64 (see kMaxGroups)
   if ((s->S + 63) / 64 * ((s->H > s->D ? s->H : s->D) / 64 + 1) >= (1 << 23))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;

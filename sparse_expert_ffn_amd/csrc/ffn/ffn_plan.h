@@ -26,6 +26,9 @@ constexpr TileCost kF32Tiles[] = {
     {64, 64, 32, 5, 300.f, 510.f, 2000.f},
 };
 constexpr int kCus = 256;
+// Workgroups of a launch: with up to 512 threads each, below 2^32 threads. The largest
+// tile stays below it for every shape that check_ffn lets through.
+constexpr int64_t kMaxGroups = (1 << 22) + (1 << 21);
 
 struct GemmPlan {
   int tile;          // index into the table
@@ -53,6 +56,7 @@ inline GemmPlan plan_gemm(bool f32, unsigned tiles, bool dual, int64_t M, int64_
     const int cols = dual ? c.bn / 2 : c.bn;
     p.tiles_n = (int)((N + cols - 1) / cols);
     const int64_t wgs = (int64_t)p.tiles_m * p.tiles_n;
+    if (wgs > kMaxGroups) continue;
     for (int s = 1; s <= 32 && s <= p.stages; ++s) {
       p.split_stages = (p.stages + s - 1) / s;
       p.splits = (p.stages + p.split_stages - 1) / p.split_stages;

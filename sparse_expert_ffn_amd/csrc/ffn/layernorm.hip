@@ -465,19 +465,15 @@ void dispatch(const LnPlan& p, F f) {
     auto it = [&](auto n) {
       if (p.tpr == decltype(tpr)::value && p.it == decltype(n)::value) f(tpr, n);
     };
-    it(std::integral_constant<int, 1>{});
-    if constexpr (VEC == 1 || decltype(tpr)::value > 64) {
-      it(std::integral_constant<int, 2>{});
-      it(std::integral_constant<int, 4>{});
-    }
-    if constexpr (decltype(tpr)::value > 64) {
-      if constexpr (VEC > 1) {
-        it(std::integral_constant<int, 3>{});
-      } else {
-        it(std::integral_constant<int, 8>{});
-        it(std::integral_constant<int, 16>{});
-      }
-    }
+    // what ln_plan can ask for: longer rows begin where the smaller group's end
+    constexpr int TPR = decltype(tpr)::value;
+    constexpr bool V = VEC > 1;
+    if constexpr (V ? TPR <= 256 : TPR == 64) it(std::integral_constant<int, 1>{});
+    if constexpr (V ? TPR == 256 : TPR <= 256) it(std::integral_constant<int, 2>{});
+    if constexpr (V && TPR >= 256) it(std::integral_constant<int, 3>{});
+    if constexpr (V ? TPR >= 256 : TPR <= 256) it(std::integral_constant<int, 4>{});
+    if constexpr (!V && TPR == 256) it(std::integral_constant<int, 8>{});
+    if constexpr (!V && TPR >= 256) it(std::integral_constant<int, 16>{});
   };
   with(std::integral_constant<int, 64>{});
   with(std::integral_constant<int, 256>{});

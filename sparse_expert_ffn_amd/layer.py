@@ -148,6 +148,8 @@ class FFNBuffers:
 
     def backward(self, dO, X, W_up, W_gate, W_down, U=None, G=None, stream=None):
         """(dX, dW_up, dW_gate, dW_down); U and G: by default the last forward's."""
+        if not hasattr(self, "dX"):
+            raise ValueError("FFNBuffers without train=True have no backward pass")
         moe_ffn_backward(self.shape, dO, X, W_up, W_gate, W_down, self.U if U is None else U,
                          self.G if G is None else G, self.dX, self.dW_up, self.dW_gate,
                          self.dW_down, self.ws, stream)

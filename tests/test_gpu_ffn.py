@@ -15,7 +15,15 @@ MD = {BF: moe.MOE_BF16, F32: moe.MOE_F32}
 # a stage, long K (splits), more rows than K
 SHAPES = [(1, 8, 8), (1, 2048, 768), (3, 72, 40), (16, 64, 64), (17, 200, 136),
           (64, 128, 256), (65, 264, 520), (130, 2056, 72), (256, 256, 256), (257, 520, 1032),
-          (300, 72, 2056), (1000, 256, 384), (2049, 64, 136), (100, 4096, 1024)]
+          (300, 72, 2056), (1000, 256, 384), (2049, 64, 136), (100, 4096, 1024),
+          (2048, 1024, 2048)]
+# every tile of every product, with and without splits of K (the plan's choices at
+# these sizes), whole and cut off in both directions
+TILES = [(1, 1032, 2056), (1, 2056, 2056), (1, 2056, 4104), (17, 1032, 2056), (17, 2056, 1032),
+         (60, 7168, 2056), (65, 2056, 4104), (65, 4104, 2056), (130, 1032, 2056), (130, 2056, 2056),
+         (1025, 72, 2056), (1025, 136, 4104), (1025, 2056, 264), (1025, 4104, 72),
+         (1025, 4104, 136), (1025, 4104, 2056), (2049, 72, 4104), (2049, 136, 72),
+         (2049, 4104, 72), (4100, 72, 2056), (4100, 136, 2056), (4100, 2056, 72)]
 
 
 def make(S, H, D, t, seed):
@@ -30,7 +38,7 @@ def rounded(ref, e, t):
 
 
 @pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("S,H,D", SHAPES)
+@pytest.mark.parametrize("S,H,D", SHAPES + TILES)
 def test_forward(S, H, D, t):
     print(f"[ffn forward {S}x{H}x{D} {t}]", flush=True)
     x, wu, wg, wd, _ = make(S, H, D, t, 1)
@@ -47,7 +55,7 @@ def test_forward(S, H, D, t):
 
 
 @pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("S,H,D", SHAPES)
+@pytest.mark.parametrize("S,H,D", SHAPES + TILES)
 def test_backward(S, H, D, t):
     print(f"[ffn backward {S}x{H}x{D} {t}]", flush=True)
     x, wu, wg, wd, do = make(S, H, D, t, 2)
@@ -61,10 +69,15 @@ def test_backward(S, H, D, t):
     first = [v.clone() for v in got]
     got = b.backward(do, x, wu, wg, wd, u, g)
     assert all(torch.equal(p, q) for p, q in zip(first, got)), "not reproducible"
+    # weight gradients as fp32: the same sums, not rounded
+    f = FFNBuffers(S, H, D, MD[t], train=True, out_f32=True, device=DEV)
+    got = f.backward(do, x, wu, wg, wd, u, g)
+    assert got[1].dtype == F32 and torch.equal(got[0], first[0])
+    assert all(torch.equal(p.to(t), q) for p, q in zip(got[1:], first[1:]))
 
 
-def test_backward_parts_and_fp32_weight_gradients():
-    """dX alone, the weight gradients alone, and those as fp32: the same values."""
+def test_backward_parts():
+    """dX alone and the weight gradients alone: the same values."""
     S, H, D = 200, 264, 392
     x, wu, wg, wd, do = make(S, H, D, BF, 3)
     u, g = mm(x, wu).to(BF), mm(x, wg).to(BF)
@@ -79,10 +92,6 @@ def test_backward_parts_and_fp32_weight_gradients():
                          b.ws)
     assert bool(torch.isnan(b.dX).all())
     assert all(torch.equal(p, q) for p, q in zip((b.dW_up, b.dW_gate, b.dW_down), want[1:]))
-    f = FFNBuffers(S, H, D, train=True, out_f32=True, device=DEV)
-    got = f.backward(do, x, wu, wg, wd, u, g)
-    assert got[1].dtype == F32 and torch.equal(got[0], want[0])
-    assert all(torch.equal(p.to(BF), q) for p, q in zip(got[1:], want[1:]))
 
 
 def test_no_tokens():

@@ -14,7 +14,10 @@ MD = {BF: moe.MOE_BF16, F32: moe.MOE_F32}
 # kernels (bf16: 2048, 16384; fp32: 1024, 8192; element-wise: 512, 4096), longer rows
 SHAPES = [(1, 1), (5, 3), (64, 8), (3, 40), (7, 511), (9, 512), (4, 513), (130, 1001),
           (33, 1024), (6, 1032), (17, 2048), (5, 2056), (3, 4097), (2, 8192), (3, 8200),
-          (2, 16384), (3, 16392), (2, 20001), (1, 65544), (3000, 72), (1025, 264)]
+          (2, 16384), (3, 16392), (2, 20001), (1, 65544), (3000, 72), (1025, 264),
+          # each number of vectors or elements per thread in between
+          (9, 101), (9, 201), (6, 301), (5, 701), (4, 1501), (4, 2501), (3, 5001), (3, 3600),
+          (3, 5000), (3, 6200), (2, 9600), (2, 12800)]
 
 
 def make(S, H, t, seed):
