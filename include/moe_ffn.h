@@ -10,8 +10,9 @@
  *  - Workspaces may hold anything before a call. Calls that may run at the
  *    same time (other streams, graphs replayed at once) need workspaces and
  *    outputs of their own. Everything can be captured in a HIP graph.
- *  - No output may overlap an input or another output (MOE_ERR_INVALID_ARGUMENT
- *    where the overlap is two equal pointers; other overlaps are not looked for).
+ *  - No output and no workspace in use may overlap an input or another output
+ *    (MOE_ERR_INVALID_ARGUMENT where the overlap is two equal pointers; other
+ *    overlaps are not looked for).
  *  - Results are bit-reproducible: every sum runs in a fixed order for a given
  *    shape, none through atomics.
  *  - NaN and infinity in an input reach the outputs that depend on it, and no
@@ -31,8 +32,10 @@ extern "C" {
  *   m_s = (1/H) sum_h X_sh,  v_s = (1/H) sum_h (X_sh - m_s)^2,  r_s = 1 / sqrt(v_s + eps)
  *   Y_sh = (X_sh - m_s) r_s gamma_h + beta_h
  * dtype MOE_F32 or MOE_BF16 (X, gamma, beta, Y); statistics and sums are fp32,
- * Y is rounded once. Any S >= 0 and H >= 1; rows whose length or base is not a
- * multiple of 16 bytes take element-wise loads.
+ * Y is rounded once. Any S from 0 and H from 1 on, S below 2^31 - 1, H below 2^27
+ * (else MOE_ERR_UNSUPPORTED, as for arrays off their element's alignment or a
+ * workspace off 16 bytes); rows whose length or base is not a multiple of 16 bytes
+ * take element-wise loads.
  *   gamma, beta  [H] dtype, each may be NULL (1 and 0)
  *   mean, rstd   [S] fp32 out, both or neither NULL (kept for the backward pass)
  * eps must be finite and >= 0.
@@ -96,7 +99,7 @@ moe_status moe_ffn_forward(const moe_ffn_shape* shape, const void* X, const void
  * is trained); the three weight gradients may be NULL together (frozen
  * weights). Sums are fp32; in bf16 mode dU, dG and h are rounded once to bf16
  * as operands of the products, whose results are rounded once.
- * Requirements as moe_ffn_forward.
+ * Requirements as moe_ffn_forward; H / 64 times D / 64 stays below 2^23 too.
  */
 size_t moe_ffn_backward_workspace_bytes(const moe_ffn_shape* shape); /* 0 if unsupported */
 moe_status moe_ffn_backward(const moe_ffn_shape* shape, const void* dO, const void* X,
@@ -159,9 +162,9 @@ moe_status moe_w4_matvec(int64_t S, int64_t K, int64_t N, int64_t E, int32_t gro
  * without an expert (it contributes nothing, whatever its weight), a token
  * whose slots are all empty (padding) and no shared expert gives a row of
  * zeros. An expert's weights are read once per 16 of its rows.
- *   shape     dtype MOE_BF16, capacity 0, flags 0 or MOE_OUTPUT_F32, S * k and S at
- *             most 4096, A and the h rows below 2 GiB; block_size and renormalize
- *             are not looked at
+ *   shape     dtype MOE_BF16, capacity 0, flags 0 or MOE_OUTPUT_F32, E at most 1024,
+ *             k at most 32, S * k and S at most 4096, A and the h rows below 2 GiB;
+ *             block_size and renormalize are not looked at
  *   A         [S][H] bf16;  W_up, W_gate: packed [E][H][D];  W_down: packed [E][D][H];
  *   Ws_*      packed with E = 1 ([H][D_shared] twice, [D_shared][H]), NULL iff D_shared = 0
  *   O         [S][H] bf16, or fp32 with MOE_OUTPUT_F32

@@ -7,6 +7,13 @@
 namespace moe {
 namespace {
 
+moe_status check_backward(const moe_ffn_shape* s) {
+  const moe_status st = check_ffn(s);
+  if (st != MOE_OK) return st;
+  // the weight gradients' tiles run over H x D
+  return (s->H + 63) / 64 * (s->D / 64 + 1) >= (1 << 23) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
 struct BwdPlan {
   GemmPlan dh, dx, dw, dwd;
   size_t du, dg, h, part, total;
@@ -91,7 +98,7 @@ void backward_t(const moe_ffn_shape* s, const BwdPlan& p, const void* dO, const 
 using namespace moe;
 
 extern "C" size_t moe_ffn_backward_workspace_bytes(const moe_ffn_shape* shape) {
-  return check_ffn(shape) == MOE_OK ? plan_backward(shape).total : 0;
+  return check_backward(shape) == MOE_OK ? plan_backward(shape).total : 0;
 }
 
 extern "C" moe_status moe_ffn_backward(const moe_ffn_shape* s, const void* dO, const void* X,
@@ -99,26 +106,19 @@ extern "C" moe_status moe_ffn_backward(const moe_ffn_shape* s, const void* dO, c
                                        const void* U, const void* G, void* dX, void* dW_up,
                                        void* dW_gate, void* dW_down, void* workspace,
                                        size_t workspace_bytes, void* stream) {
-  const moe_status st = check_ffn(s);
+  const moe_status st = check_backward(s);
   if (st != MOE_OK) return st;
-  // the weight gradients' tiles run over H x D
-  if ((s->H + 63) / 64 * (s->D / 64 + 1) >= (1 << 23)) return MOE_ERR_UNSUPPORTED;
   if ((dW_up == nullptr) != (dW_gate == nullptr) || (dW_up == nullptr) != (dW_down == nullptr) ||
       (dX == nullptr && dW_up == nullptr && s->S > 0))
     return MOE_ERR_INVALID_ARGUMENT;
-  const void* in[] = {dO, X, W_up, W_gate, W_down, U, G};
-  const void* out[] = {dX, dW_up, dW_gate, dW_down, workspace};
-  for (int i = 0; i < 5; ++i) {
-    if (!ffn_aligned16(out[i])) return MOE_ERR_UNSUPPORTED;
-    for (const void* q : in)
-      if (out[i] != nullptr && out[i] == q) return MOE_ERR_INVALID_ARGUMENT;
-    for (int j = 0; j < i; ++j)
-      if (out[i] != nullptr && out[i] == out[j]) return MOE_ERR_INVALID_ARGUMENT;
-  }
-  for (const void* q : in) {
+  if (ffn_shared({dX, dW_up, dW_gate, dW_down, workspace}, {dO, X, W_up, W_gate, W_down, U, G}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  for (const void* q : {dO, X, W_up, W_gate, W_down, U, G}) {
     if (q == nullptr && s->S > 0) return MOE_ERR_INVALID_ARGUMENT;
     if (!ffn_aligned16(q)) return MOE_ERR_UNSUPPORTED;
   }
+  for (const void* q : {dX, dW_up, dW_gate, dW_down, workspace})
+    if (!ffn_aligned16(q)) return MOE_ERR_UNSUPPORTED;
   hipStream_t q = (hipStream_t)stream;
   const bool wf32 = s->dtype == MOE_F32 || (s->flags & MOE_OUTPUT_F32) != 0;
   if (s->S == 0) {

@@ -1,6 +1,8 @@
 // Definitions shared by the operators declared in include/moe_ffn.h.
 #pragma once
 
+#include <initializer_list>
+
 #include "moe_common.h"
 #include "moe_ffn.h"
 
@@ -9,12 +11,19 @@ namespace moe {
 inline size_t ffn_round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool ffn_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// 16 bytes as T elements.
-template <typename T>
-struct Vec16 {
-  static constexpr int N = 16 / (int)sizeof(T);
-  T v[N];
-};
+// Whether an output (or workspace) is also an input or another output; absent ones
+// (null) are not.
+inline bool ffn_shared(std::initializer_list<const void*> outs,
+                       std::initializer_list<const void*> ins) {
+  for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+    if (*o == nullptr) continue;
+    for (const void* q : ins)
+      if (*o == q) return true;
+    for (const void* const* p = outs.begin(); p != o; ++p)
+      if (*o == *p) return true;
+  }
+  return false;
+}
 
 // 4 consecutive floats.
 __device__ __forceinline__ f32x4_t load4(const float* p) {

@@ -98,15 +98,10 @@ extern "C" moe_status moe_ffn_forward(const moe_ffn_shape* s, const void* X, con
   if (s->S == 0) return MOE_OK;
   if (X == nullptr || W_up == nullptr || W_gate == nullptr || W_down == nullptr || O == nullptr)
     return MOE_ERR_INVALID_ARGUMENT;
-  const void* out[] = {O, U, G, workspace};
-  for (int i = 0; i < 4; ++i) {
-    if (!ffn_aligned16(out[i])) return MOE_ERR_UNSUPPORTED;
-    for (const void* q : {X, W_up, W_gate, W_down})
-      if (out[i] != nullptr && out[i] == q) return MOE_ERR_INVALID_ARGUMENT;
-    for (int j = 0; j < i; ++j)
-      if (out[i] != nullptr && out[i] == out[j]) return MOE_ERR_INVALID_ARGUMENT;
-  }
-  for (const void* q : {X, W_up, W_gate, W_down})
+  if (ffn_shared({O, U, G, workspace}, {X, W_up, W_gate, W_down}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  for (const void* q : {X, W_up, W_gate, W_down, (const void*)O, (const void*)U, (const void*)G,
+                        (const void*)workspace})
     if (!ffn_aligned16(q)) return MOE_ERR_UNSUPPORTED;
   const FwdPlan p = plan_forward(s);
   if (workspace == nullptr || workspace_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;

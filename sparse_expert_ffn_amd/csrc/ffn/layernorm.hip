@@ -21,6 +21,7 @@
 namespace moe {
 namespace {
 
+constexpr int64_t kMaxRow = 1 << 27;
 constexpr int kThreads = 256;  // of the kernels that share rows by waves, or re-read them
 
 template <int CTRL>
@@ -522,7 +523,8 @@ moe_status check_ln(int64_t S, int64_t H, int32_t dtype) {
   if (S < 0 || H < 1) return MOE_ERR_INVALID_ARGUMENT;
   if (dtype == MOE_MXFP8) return MOE_ERR_UNSUPPORTED;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARGUMENT;
-  if (S >= INT32_MAX || H >= INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  // the column sums' launch: 32 H threads, below 2^32
+  if (S >= INT32_MAX || H >= kMaxRow) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -543,7 +545,8 @@ extern "C" moe_status moe_layernorm_forward(int64_t S, int64_t H, int32_t dtype,
   if (!(eps >= 0.f) || eps > 3.0e38f) return MOE_ERR_INVALID_ARGUMENT;
   if ((mean == nullptr) != (rstd == nullptr)) return MOE_ERR_INVALID_ARGUMENT;
   if (S == 0) return MOE_OK;
-  if (X == nullptr || Y == nullptr || X == Y) return MOE_ERR_INVALID_ARGUMENT;
+  if (X == nullptr || Y == nullptr || ffn_shared({Y, mean, rstd}, {X, gamma, beta}))
+    return MOE_ERR_INVALID_ARGUMENT;
   const int es = dtype == MOE_F32 ? 4 : 2;
   if (misaligned(X, es) || misaligned(Y, es) || misaligned(gamma, es) || misaligned(beta, es) ||
       misaligned(mean, 4) || misaligned(rstd, 4))
@@ -585,12 +588,14 @@ extern "C" moe_status moe_layernorm_backward(int64_t S, int64_t H, int32_t dtype
   if (st != MOE_OK) return st;
   if ((dgamma == nullptr) != (dbeta == nullptr)) return MOE_ERR_INVALID_ARGUMENT;
   if (S > 0 && (dY == nullptr || X == nullptr || mean == nullptr || rstd == nullptr ||
-                dX == nullptr || dX == dY || dX == X))
+                dX == nullptr))
     return MOE_ERR_INVALID_ARGUMENT;
-  if (dgamma != nullptr && (workspace == nullptr || dgamma == dbeta))
-    return workspace == nullptr ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_ERR_INVALID_ARGUMENT;
+  if (ffn_shared({dX, dgamma, dbeta, dgamma != nullptr ? workspace : nullptr},
+                 {dY, X, gamma, mean, rstd}))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (dgamma != nullptr &&
-      workspace_bytes < moe_layernorm_backward_workspace_bytes(S, H, dtype))
+      (workspace == nullptr ||
+       workspace_bytes < moe_layernorm_backward_workspace_bytes(S, H, dtype)))
     return MOE_ERR_WORKSPACE_TOO_SMALL;
   const int es = dtype == MOE_F32 ? 4 : 2;
   if (misaligned(X, es) || misaligned(dY, es) || misaligned(dX, es) || misaligned(gamma, es) ||

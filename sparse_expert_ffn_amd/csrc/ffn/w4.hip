@@ -536,7 +536,8 @@ extern "C" moe_status moe_quantize_w4(const void* W, int64_t E, int64_t K, int64
   const moe_status st = check_w4(E, K, N, group);
   if (st != MOE_OK) return st;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARGUMENT;
-  if (W == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (W == nullptr || codes == nullptr || scales == nullptr || ffn_shared({codes, scales}, {W}))
+    return MOE_ERR_INVALID_ARGUMENT;
   const int es = dtype == MOE_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(W) % es || reinterpret_cast<uintptr_t>(scales) % 2)
     return MOE_ERR_UNSUPPORTED;
@@ -558,7 +559,7 @@ extern "C" moe_status moe_pack_w4_weights(const uint8_t* codes, const void* scal
   const moe_status st = check_w4(E, K, N, group);
   if (st != MOE_OK) return st;
   if (codes == nullptr || scales == nullptr || packed == nullptr ||
-      (const void*)codes == scales || packed == (const void*)codes || packed == scales)
+      ffn_shared({packed, scales}, {codes}))
     return MOE_ERR_INVALID_ARGUMENT;
   if (!ffn_aligned16(packed) || reinterpret_cast<uintptr_t>(scales) % 2)
     return MOE_ERR_UNSUPPORTED;
@@ -577,7 +578,7 @@ extern "C" moe_status moe_w4_matvec(int64_t S, int64_t K, int64_t N, int64_t E, 
   if (st != MOE_OK) return st;
   if (S > kMaxRows || S * K * 2 >= kMaxBytes) return MOE_ERR_UNSUPPORTED;
   if (S == 0) return MOE_OK;
-  if (X == nullptr || W == nullptr || Y == nullptr || X == Y || W == Y)
+  if (X == nullptr || W == nullptr || Y == nullptr || ffn_shared({Y}, {X, W, expert_ids}))
     return MOE_ERR_INVALID_ARGUMENT;
   if (!ffn_aligned16(X) || !ffn_aligned16(W) || !ffn_aligned16(Y) ||
       reinterpret_cast<uintptr_t>(expert_ids) % 4)
@@ -615,7 +616,9 @@ extern "C" moe_status moe_w4_forward(const moe_shape* s, int32_t group, const vo
   if (!group_ok(group)) return MOE_ERR_INVALID_ARGUMENT;
   if (s->S == 0) return MOE_OK;
   if (A == nullptr || W_up == nullptr || W_gate == nullptr || W_down == nullptr ||
-      topk_ids == nullptr || topk_weights == nullptr || O == nullptr || O == A)
+      topk_ids == nullptr || topk_weights == nullptr || O == nullptr ||
+      ffn_shared({O, workspace}, {A, W_up, W_gate, W_down, Ws_up, Ws_gate, Ws_down, topk_ids,
+                                  topk_weights}))
     return MOE_ERR_INVALID_ARGUMENT;
   const bool sh = s->D_shared > 0;
   if ((Ws_up != nullptr) != sh || (Ws_gate != nullptr) != sh || (Ws_down != nullptr) != sh)

@@ -271,11 +271,17 @@ def moe_pack_w4_weights(codes, scales, group, packed, stream=None, check=True) -
                  a("packed", packed, (need,) if need else None, torch.uint8))
 
 
+def _w4_weight(call, name, w):
+    if not hasattr(w, "packed"):
+        raise TypeError(f"{call}: {name} must be a W4Weight, not {type(w).__name__}")
+
+
 def moe_w4_matvec(X, W, Y, expert_ids=None, stream=None, check=True) -> int:
     """Y = X W for few rows X [S][K] (bfloat16) and a packed weight W
     (layer.W4Weight); Y [S][N] bfloat16 or float32; expert_ids [S] int32: the
     matrix each row takes (none: row of zeros)."""
     a = _Args("moe_w4_matvec")
+    _w4_weight(a.call, "W", W)
     S, K = _matrix(a.call, "X", X)
     if K != W.K:
         raise ValueError(f"moe_w4_matvec: X has {K} columns, W {W.K} rows")
@@ -297,11 +303,14 @@ def moe_w4_forward(shape, A, W_up, W_gate, W_down, Ws_up, Ws_gate, Ws_down, topk
     topk_weights."""
     a = _Args("moe_w4_forward")
     S, H, D, Ds, E, k = (shape.S, shape.H, shape.D, shape.D_shared, shape.E, shape.k)
+    for name, w in (("W_up", W_up), ("W_gate", W_gate), ("W_down", W_down)):
+        _w4_weight(a.call, name, w)
     group = W_up.group
 
     def packed(name, w, want):
         if w is None:
             return None
+        _w4_weight(a.call, name, w)
         if (w.E, w.K, w.N, w.group) != want + (group,):
             raise ValueError(f"{a.call}: {name} is {w}, not {want} in groups of {group}")
         return a(name, w.packed, (w.nbytes,), torch.uint8)

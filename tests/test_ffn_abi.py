@@ -10,6 +10,7 @@ import torch
 
 import sparse_expert_ffn_amd as moe
 from sparse_expert_ffn_amd import buildlib, ffn
+from sparse_expert_ffn_amd.layer import W4Weight
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A = [0x100000 * (i + 1) for i in range(20)]  # distinct aligned addresses, never dereferenced
@@ -211,6 +212,61 @@ def test_w4_forward_refusals(lib):
     assert f(n=need - 1) == SMALL and f(over=dict(ws=None)) == SMALL
     assert moe.moe_w4_forward_workspace_bytes(moe.make_shape(4, 64, 128, 8, 2, capacity=1)) == 0
     assert f(S=0, over=dict(A=None, O=None, ids=None, w=None)) == OK
+
+
+def test_an_output_that_is_another_array_is_refused(lib):
+    """Two equal pointers, one of them an output's or the workspace's, in every pair."""
+    def pairs(call, names, outs):
+        for a in outs:
+            for b in names:
+                if a != b:
+                    assert call(**{a: A[14], b: A[14]}) == INVALID, (a, b)
+
+    pairs(lambda **k: ln_fwd(lib, **k), "X g b Y m r".split(), "Y m r".split())
+    pairs(lambda **k: ln_bwd(lib, **k), "dY X g m r dX dg db ws".split(), "dX dg db ws".split())
+    pairs(lambda **k: ffn_fwd(lib, **k), "X Wu Wg Wd U G O ws".split(), "U G O ws".split())
+    pairs(lambda **k: ffn_bwd(lib, **k), "dO X Wu Wg Wd U G dX dWu dWg dWd ws".split(),
+          "dX dWu dWg dWd ws".split())
+
+    def quantize(W=A[0], c=A[1], s=A[2]):
+        return lib.moe_quantize_w4(W, 1, 128, 16, BF, 32, c, s, None)
+
+    def pack(c=A[0], s=A[1], o=A[2]):
+        return lib.moe_pack_w4_weights(c, s, 1, 128, 16, 32, o, None)
+
+    def matvec(X=A[0], W=A[1], ids=A[2], Y=A[3]):
+        return lib.moe_w4_matvec(1, 128, 16, 1, 32, 0, X, W, ids, Y, None)
+
+    def layer(**kw):
+        s = moe.make_shape(4, 64, 128, 8, 2, 64)
+        names = ["A", "Wu", "Wg", "Wd", "Su", "Sg", "Sd", "ids", "w", "O", "ws"]
+        return lib.moe_w4_forward(ctypes.byref(s), 32,
+                                  *[kw.get(n, A[i]) for i, n in enumerate(names)], 1 << 40, None)
+
+    pairs(quantize, "W c s".split(), "c s".split())
+    pairs(pack, "c s o".split(), ["o"])
+    pairs(matvec, "X W ids Y".split(), ["Y"])
+    pairs(layer, "A Wu Wg Wd Su Sg Sd ids w O ws".split(), "O ws".split())
+
+
+def test_sizes_past_a_launch_are_refused(lib):
+    assert ln_fwd(lib, H=1 << 27) == UNSUPPORTED
+    assert ln_bwd(lib, S=1, H=1 << 27) == UNSUPPORTED
+    assert moe.moe_layernorm_backward_workspace_bytes(1, 1 << 27, F32) == 0
+    wide = dict(S=16, H=1 << 21, D=1 << 21)   # H x D gradients of 2^30 tiles
+    assert ffn_bwd(lib, **wide) == UNSUPPORTED
+    assert moe.moe_ffn_backward_workspace_bytes(moe.make_ffn_shape(**wide)) == 0
+
+
+def test_binding_names_a_missing_weight():
+    x = torch.zeros(4, 64)
+    with pytest.raises(TypeError, match="W must be a W4Weight"):
+        moe.moe_w4_matvec(x, None, x)
+    with pytest.raises(TypeError, match="W_up must be a W4Weight"):
+        moe.moe_w4_forward(moe.make_shape(4, 64, 128, 8, 2), x, None, None, None, None, None,
+                           None, x, x, x, None)
+    with pytest.raises(ValueError, match="group"):
+        W4Weight.quantize(x, group=0)
 
 
 def test_binding_refuses_bad_tensors():
