@@ -158,7 +158,8 @@ class FFNBuffers:
 
 class W4Weight:
     """A weight [E][K][N] or [K][N] as 4-bit codes and group scales, packed for the
-    products (codes and scales are not kept)."""
+    products (codes and scales are not kept). With a stream, codes and scales have to
+    live until its work is done."""
 
     def __init__(self, codes, scales, group=128, stream=None):
         self.E, self.K, self.N = (1, *codes.shape) if codes.dim() == 2 else tuple(codes.shape)
@@ -171,11 +172,18 @@ class W4Weight:
     def quantize(cls, W, group=128, stream=None):
         """The library's quantisation of a bf16 or fp32 tensor."""
         K, N = W.shape[-2:]
-        codes = torch.empty(W.shape, dtype=torch.uint8, device=W.device)
-        scales = torch.empty((*W.shape[:-2], -(-K // group), N), dtype=torch.bfloat16,
-                             device=W.device)
-        moe_quantize_w4(W, group, codes, scales, stream)
-        return cls(codes, scales, group, stream)
+        if group < 1:
+            raise ValueError(f"W4Weight.quantize: group is {group}, not 32, 64 or 128")
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=W.device)
+        # the codes and scales are given back when this returns: they belong to the
+        # stream that the two calls run on, so that nothing reuses them before
+        with torch.cuda.stream(stream):
+            codes = torch.empty(W.shape, dtype=torch.uint8, device=W.device)
+            scales = torch.empty((*W.shape[:-2], -(-K // group), N), dtype=torch.bfloat16,
+                                 device=W.device)
+            moe_quantize_w4(W, group, codes, scales, stream)
+            return cls(codes, scales, group, stream)
 
     def __repr__(self):
         return f"W4Weight(E={self.E}, K={self.K}, N={self.N}, group={self.group})"

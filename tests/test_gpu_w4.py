@@ -274,3 +274,37 @@ def test_binding_refusals():
     b = W4MoEBuffers(2, 64, 16, 2, 1, group=32, device=DEV)
     with pytest.raises(ValueError, match="W_down"):
         b.forward(x, w, w, w)
+
+
+@pytest.mark.parametrize("as_int", [False, True], ids=["stream", "handle"])
+def test_quantize_on_another_stream(as_int):
+    """What quantize allocates on the way is not reused while that stream's work runs."""
+    W = normal(gen(12), (4, 512, 256), 0.05, BF)
+    want = W4Weight.quantize(W, 64).packed.clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):  # work ahead of it: some milliseconds
+        a = torch.ones((4096, 4096), device=DEV)
+        for _ in range(20):
+            a = a @ a * 0.0
+    w = W4Weight.quantize(W, 64, stream=side.cuda_stream if as_int else side)
+    junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+            for n in (W.numel(), W.numel() // 32) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(w.packed, want) and len(junk) == 8
+
+
+def test_layer_many_slots():
+    """More slots to a token than the combine loads at a time, few tokens and many."""
+    g = gen(13)
+    H, D, E, k, group = 64, 40, 24, 19, 32
+    up, gate, down = w4(g, E, H, D, group), w4(g, E, H, D, group), w4(g, E, D, H, group)
+    packed = [W4Weight(*p, group=group) for p in (up, gate, down)]
+    for S in (1, 30):
+        x = normal(g, (S, H), 1.0, BF)
+        b = W4MoEBuffers(S, H, D, E, k, group=group, out_f32=True, device=DEV)
+        b.route(logits_in=torch.randn((S, E), generator=g, device=DEV))
+        b.topk_ids[0, 8] = -1
+        o = b.forward(x, *packed)
+        ref, e = layer_ref(x, up, gate, down, None, b.topk_ids, b.topk_weights, group)
+        check("o", o, ref, e + half(F32) * ref.abs())
