@@ -10,6 +10,11 @@ namespace moe {
 // holds, and its times in ns, fitted to measured products (16384 x 2048 x 4096 down to
 // 64 x 2048 x 768): a CU that runs n of them takes wait + n busy for a K stage of each;
 // fixed is what a workgroup takes beyond its stages (launch, first loads, epilogue).
+// The 16-row tiles are for few rows, where the other tiles' MFMAs on rows that are not
+// there take longer than the weights' way in (fp32, 1 x 7168 x 2048: up and gate 37 ->
+// 22 us, down 22 -> 13 us), and for products of few tiles in all (64 x 128 x 256 fp32:
+// down in one launch at 6.8 us instead of 4.3 and a join of 2.9); 3 rows of them instead
+// of one of 64 are slower (48 x 512 x 512 fp32: 21 against 16 us with joins).
 struct TileCost {
   int bm, bn, bk, per_cu;
   float wait_ns, busy_ns, fixed_ns;
@@ -24,6 +29,7 @@ constexpr TileCost kBfTiles[] = {
 constexpr TileCost kF32Tiles[] = {
     {128, 128, 32, 2, 70.f, 2130.f, 2500.f},
     {64, 64, 32, 5, 300.f, 510.f, 2000.f},
+    {16, 64, 32, 5, 250.f, 350.f, 2300.f},
 };
 constexpr int kCus = 256;
 // Workgroups of a launch: with up to 512 threads each, below 2^32 threads. The largest
@@ -45,7 +51,7 @@ inline GemmPlan plan_gemm(bool f32, unsigned tiles, bool dual, int64_t M, int64_
                           int pairs) {
   GemmPlan best = {};
   float best_ns = 3.0e38f;
-  const int n = f32 ? 2 : 5;
+  const int n = f32 ? 3 : 5;
   for (int t = 0; t < n; ++t) {
     if (!(tiles >> t & 1)) continue;
     const TileCost& c = f32 ? kF32Tiles[t] : kBfTiles[t];
@@ -106,16 +112,25 @@ void launch_tile(const GemmArgs& g, const EP& ep, hipStream_t st) {
 // The tiles of a product with these operand orders.
 template <bool DUAL, bool AKC, bool BKC>
 constexpr unsigned tile_mask(bool f32) {
-  return f32 ? 3u : AKC ? 31u : 23u;  // 16 rows: K-contiguous A only
+  return f32 ? (AKC ? 7u : 3u) : AKC ? 31u : 23u;  // 16 rows: K-contiguous A only
 }
 
 template <typename T, bool DUAL, bool AKC, bool BKC, typename EP>
 void launch_gemm(const GemmPlan& p, const GemmArgs& g, const EP& ep, hipStream_t st) {
   constexpr int NP = DUAL ? 2 : 1;
   if constexpr (sizeof(T) == 4) {
-    if (p.tile == 0)
+    if (p.tile == 0) {
       launch_tile<TileCore<T, 128, 128, 2, DUAL, AKC, BKC, 2, 4, 2>>(g, ep, st);
-    else
+      return;
+    }
+    if constexpr (AKC)
+      if (p.tile == 2) {
+        if (p.tiles_m == 1)
+          launch_tile<TileCore<T, 16, 64, NP, DUAL, AKC, BKC, 1, 2, 3, true>>(g, ep, st);
+        else
+          launch_tile<TileCore<T, 16, 64, NP, DUAL, AKC, BKC, 1, 2, 3>>(g, ep, st);
+        return;
+      }
       launch_tile<TileCore<T, 64, 64, NP, DUAL, AKC, BKC, 2, 2, 2>>(g, ep, st);
   } else {
     if (p.tile == 0)
