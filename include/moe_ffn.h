@@ -34,8 +34,8 @@ extern "C" {
  * dtype MOE_F32 or MOE_BF16 (X, gamma, beta, Y); statistics and sums are fp32,
  * Y is rounded once. Any S from 0 and H from 1 on, S below 2^31 - 1, H below 2^27
  * (else MOE_ERR_UNSUPPORTED, as for arrays off their element's alignment or a
- * workspace off 16 bytes); rows whose length or base is not a multiple of 16 bytes
- * take element-wise loads.
+ * workspace off 16 bytes); arrays whose rows are whole 16-byte vectors
+ * and aligned to them are fastest.
  *   gamma, beta  [H] dtype, each may be NULL (1 and 0)
  *   mean, rstd   [S] fp32 out, both or neither NULL (kept for the backward pass)
  * eps must be finite and >= 0.

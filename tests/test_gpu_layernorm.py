@@ -17,7 +17,11 @@ SHAPES = [(1, 1), (5, 3), (64, 8), (3, 40), (7, 511), (9, 512), (4, 513), (130, 
           (2, 16384), (3, 16392), (2, 20001), (1, 65544), (3000, 72), (1025, 264),
           # each number of vectors or elements per thread in between
           (9, 101), (9, 201), (6, 301), (5, 701), (4, 1501), (4, 2501), (3, 5001), (3, 3600),
-          (3, 5000), (3, 6200), (2, 9600), (2, 12800)]
+          (3, 5000), (3, 6200), (2, 9600), (2, 12800),
+          # rows that end inside a vector, of every kernel; rows shorter than a vector;
+          # groups of several rows
+          (3, 3601), (3, 7001), (2, 9001), (2, 13001), (40, 5), (300, 2), (5000, 7), (9, 65),
+          (2000, 33), (9, 129), (9, 257), (700, 2049), (600, 1003), (2100, 520), (530, 9001)]
 
 
 def make(S, H, t, seed):
@@ -88,6 +92,28 @@ def test_arrays_off_16_bytes(t, H):
     check("dx", dx, rx, ex + half(t) * (rx.abs() + ex))
     check("dgamma", dg, rg, eg)
     check("dbeta", db, rb, eb)
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("S,H", [(1, 1), (3, 3), (37, 7), (5, 33), (130, 130), (6, 511), (3, 2049),
+                                 (2, 9001), (2, 20001), (3, 64), (600, 1000)])
+def test_nothing_beside_the_outputs_is_written(S, H, t):
+    x, gamma, beta, dy = make(S, H, t, 6)
+    n = moe.moe_layernorm_backward_workspace_bytes(S, H, MD[t])
+    pad = 64  # elements or bytes on either side
+
+    def framed(shape, dtype):
+        size = int(torch.tensor(shape).prod())
+        b = torch.full((size + 2 * pad,), 7, dtype=dtype, device=DEV)
+        return b, b[pad:pad + size].view(shape)
+
+    out = [framed((S, H), t), framed((S,), F32), framed((S,), F32), framed((S, H), t),
+           framed((H,), F32), framed((H,), F32), framed((n,), torch.uint8)]
+    y, mean, rstd, dx, dg, db, ws = (v for _, v in out)
+    moe.moe_layernorm_forward(x, gamma, beta, 1e-5, y, mean, rstd)
+    moe.moe_layernorm_backward(dy, x, gamma, mean, rstd, dx, dg, db, ws)
+    for b, _ in out:
+        assert bool((b[:pad] == 7).all()) and bool((b[-pad:] == 7).all())
 
 
 def test_large_offset_keeps_the_variance():
