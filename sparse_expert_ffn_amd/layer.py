@@ -156,17 +156,34 @@ class FFNBuffers:
         return self.dX, self.dW_up, self.dW_gate, self.dW_down
 
 
+def _as_stream(stream, device):
+    """A stream's handle as a Stream; Streams and None as they are."""
+    return torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+
+
 class W4Weight:
     """A weight [E][K][N] or [K][N] as 4-bit codes and group scales, packed for the
-    products (codes and scales are not kept). With a stream, codes and scales have to
-    live until its work is done."""
+    products (codes and scales are not kept).
+
+    With a stream, the work runs there, after what it already holds: whoever fills codes
+    and scales, or reads the packed weight, on another stream has to order the two. The
+    packed weight is allocated on that stream too (a block of the current stream's pool
+    may still be in use by its work), and is not reused before the current stream's
+    work as of its release; a weight released while a third stream reads it needs
+    ``packed.record_stream`` of that one. codes, scales and W may be released at once."""
 
     def __init__(self, codes, scales, group=128, stream=None):
         self.E, self.K, self.N = (1, *codes.shape) if codes.dim() == 2 else tuple(codes.shape)
         self.group = group
         self.nbytes = moe_w4_weight_bytes(self.E, self.K, self.N, group)
-        self.packed = torch.empty(self.nbytes, dtype=torch.uint8, device=codes.device)
-        moe_pack_w4_weights(codes, scales, group, self.packed, stream)
+        stream = _as_stream(stream, codes.device)
+        with torch.cuda.stream(stream):
+            self.packed = torch.empty(self.nbytes, dtype=torch.uint8, device=codes.device)
+            moe_pack_w4_weights(codes, scales, group, self.packed, stream)
+        if stream is not None:
+            codes.record_stream(stream)
+            scales.record_stream(stream)
+            self.packed.record_stream(torch.cuda.current_stream(codes.device))
 
     @classmethod
     def quantize(cls, W, group=128, stream=None):
@@ -174,8 +191,7 @@ class W4Weight:
         K, N = W.shape[-2:]
         if group < 1:
             raise ValueError(f"W4Weight.quantize: group is {group}, not 32, 64 or 128")
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=W.device)
+        stream = _as_stream(stream, W.device)
         # the codes and scales are given back when this returns: they belong to the
         # stream that the two calls run on, so that nothing reuses them before
         with torch.cuda.stream(stream):
@@ -183,7 +199,9 @@ class W4Weight:
             scales = torch.empty((*W.shape[:-2], -(-K // group), N), dtype=torch.bfloat16,
                                  device=W.device)
             moe_quantize_w4(W, group, codes, scales, stream)
-            return cls(codes, scales, group, stream)
+        if stream is not None:
+            W.record_stream(stream)
+        return cls(codes, scales, group, stream)
 
     def __repr__(self):
         return f"W4Weight(E={self.E}, K={self.K}, N={self.N}, group={self.group})"

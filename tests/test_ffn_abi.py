@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import sparse_expert_ffn_amd as moe
-from sparse_expert_ffn_amd import buildlib, ffn
+from sparse_expert_ffn_amd import buildlib, ffn, layer
 from sparse_expert_ffn_amd.layer import W4Weight
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -286,3 +286,66 @@ def test_binding_refuses_bad_tensors():
     m = torch.empty((4, 8), device="meta")
     with pytest.raises(ValueError, match="device memory"):
         a("X", m)
+
+
+class _Streams:
+    """Stands in for torch's streams and allocations: which stream is current when memory
+    is taken and when a call is made, and which streams a tensor's memory waits for."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.calls = "reader", []
+        outer = self
+
+        class Context:
+            def __init__(self, stream):
+                self.stream = stream
+
+            def __enter__(self):
+                self.before = outer.current
+                if self.stream is not None:
+                    outer.current = self.stream
+
+            def __exit__(self, *exc):
+                outer.current = self.before
+
+        class Tensor:
+            def __init__(self, shape, owner):
+                self.shape, self.owner, self.recorded, self.device = shape, owner, set(), "cuda:0"
+
+            def dim(self):
+                return len(self.shape)
+
+            def record_stream(self, stream):
+                self.recorded.add(stream)
+
+        self.tensor = lambda *shape: Tensor(shape, self.current)
+        monkeypatch.setattr(torch.cuda, "stream", Context)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: self.current)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: f"stream {h}")
+        monkeypatch.setattr(torch, "empty", lambda shape, **kw: Tensor(
+            shape if isinstance(shape, tuple) else (shape,), self.current))
+        for name in ("moe_quantize_w4", "moe_pack_w4_weights"):
+            monkeypatch.setattr(layer, name, lambda *a, name=name: self.calls.append((name, a)))
+
+
+@pytest.mark.parametrize("stream", ["side", 77, None])
+def test_packed_weight_belongs_to_the_stream_that_writes_it(lib, monkeypatch, stream):
+    """W4Weight from codes and from a tensor: what is allocated on the way comes from the
+    pool of the stream that writes it (another stream's work may still use a block of the
+    current one's), and no argument, nor the result, is given back to a pool while one of
+    the two streams uses it."""
+    s = _Streams(monkeypatch)
+    on = {"side": "side", 77: "stream 77", None: "reader"}[stream]
+    codes, scales = s.tensor(2, 64, 16), s.tensor(2, 2, 16)
+    w = W4Weight(codes, scales, 32, stream=stream)
+    assert w.packed.owner == on and s.current == "reader"
+    if stream is not None:
+        assert codes.recorded == scales.recorded == {on} and w.packed.recorded == {"reader"}
+    W = s.tensor(2, 64, 16)
+    s.calls.clear()
+    w = W4Weight.quantize(W, 32, stream=stream)
+    assert [n for n, _ in s.calls] == ["moe_quantize_w4", "moe_pack_w4_weights"]
+    assert all(t.owner == on for t in (*s.calls[0][1][2:4], w.packed))
+    assert s.current == "reader"
+    if stream is not None:
+        assert W.recorded == {on} and w.packed.recorded == {"reader"}

@@ -308,3 +308,60 @@ def test_layer_many_slots():
         o = b.forward(x, *packed)
         ref, e = layer_ref(x, up, gate, down, None, b.topk_ids, b.topk_weights, group)
         check("o", o, ref, e + half(F32) * ref.abs())
+
+
+def _busy(n=20):
+    """Some milliseconds of work on the current stream; its result is 0."""
+    a = torch.ones((4096, 4096), device=DEV)
+    for _ in range(n):
+        a = a @ a * 0.0
+    return a[0, 0]
+
+
+@pytest.mark.parametrize("as_int", [False, True], ids=["stream", "handle"])
+def test_pack_on_another_stream(as_int):
+    """The packed weight takes no block that the current stream's work still writes, and
+    codes and scales may be released while the other stream's work reads them."""
+    codes, scales = w4(gen(14), 4, 512, 256, 64)
+    want = W4Weight(codes, scales, 64).packed.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    zero = _busy()
+    freed = torch.empty_like(want)
+    freed.copy_((zero + 255).expand(freed.shape))  # behind the work
+    del freed
+    w = W4Weight(codes, scales, 64, stream=side.cuda_stream if as_int else side)
+    torch.cuda.synchronize()
+    assert torch.equal(w.packed, want)
+    with torch.cuda.stream(side):
+        _busy()
+    w = W4Weight(codes, scales, 64, stream=side.cuda_stream if as_int else side)
+    sizes = (codes.numel(), scales.numel() * 2)
+    del codes, scales
+    junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(w.packed, want) and len(junk) == 8
+
+
+def test_released_weight_is_not_overwritten_while_it_is_read():
+    """A weight made on another stream, dropped with a product of the current stream still
+    to read it: the next weight made there does not take its place before."""
+    g = gen(15)
+    first, second = w4(g, 2, 512, 256, 64), w4(g, 2, 512, 256, 64)
+    x = normal(g, (5, 512), 1.0, BF)
+    want, y = torch.empty((5, 256), device=DEV), torch.empty((5, 256), device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    w = W4Weight(*first, 64, stream=side)
+    torch.cuda.synchronize()
+    moe.moe_w4_matvec(x, w, want)
+    torch.cuda.synchronize()
+    _busy()
+    moe.moe_w4_matvec(x, w, y)
+    del w
+    w = W4Weight(*second, 64, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    moe.moe_w4_matvec(x, w, y)
+    assert not torch.equal(y, want)
