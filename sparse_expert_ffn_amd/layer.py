@@ -209,7 +209,8 @@ class W4Weight:
 
 class W4MoEBuffers:
     """The MoE layer with 4-bit expert weights for few tokens: router, then the
-    experts (no align step)."""
+    experts (no align step). The calls run on the buffers' device, on ``stream`` or its
+    current stream."""
 
     def __init__(self, S, H, D, E, k, D_shared=0, group=128, renormalize=1, out_f32=False,
                  device="cuda"):
@@ -227,8 +228,15 @@ class W4MoEBuffers:
                               device=device)
 
     def route(self, A=None, W_router=None, router_bias=None, logits_in=None, stream=None):
-        moe_gate_topk(self.shape, A, W_router, router_bias, logits_in, self.logits,
-                      self.topk_ids, self.topk_weights, self.gate_ws, stream)
+        args = (self.shape, A, W_router, router_bias, logits_in, self.logits, self.topk_ids,
+                self.topk_weights, self.gate_ws, stream)
+        # the router's binding takes the current device and its stream, the experts' the
+        # tensors': both on the buffers' device, so that they are in order
+        if self.O.get_device() == torch.cuda.current_device():
+            moe_gate_topk(*args)
+        else:
+            with torch.cuda.device(self.O.get_device()):
+                moe_gate_topk(*args)
 
     def forward(self, A, W_up, W_gate, W_down, Ws_up=None, Ws_gate=None, Ws_down=None,
                 topk_ids=None, topk_weights=None, stream=None):

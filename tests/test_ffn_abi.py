@@ -349,3 +349,58 @@ def test_packed_weight_belongs_to_the_stream_that_writes_it(lib, monkeypatch, st
     assert s.current == "reader"
     if stream is not None:
         assert W.recorded == {on} and w.packed.recorded == {"reader"}
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_router_and_experts_run_on_the_buffers_device(lib, monkeypatch, current):
+    """W4MoEBuffers whose device is not the current one: both of the layer's calls are
+    made on it (they take the current stream of the device that they run on)."""
+    device, calls = [current], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, device[0] = device[0], self.index
+
+        def __exit__(self, *exc):
+            device[0] = self.before
+
+    class Tensor:
+        def __init__(self, shape, dtype):
+            self.shape, self.dtype, self.is_cuda, self.nbytes = shape, dtype, True, 1 << 20
+
+        def get_device(self):
+            return 1
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return A[0]
+
+    class Lib:
+        def moe_w4_forward(self, *args):
+            calls.append(("experts", device[0], args[-1]))
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: device[0])
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None: Tensor(
+        shape if isinstance(shape, tuple) else (shape,), dtype))
+    b = layer.W4MoEBuffers(4, 64, 128, 8, 2, group=32, device="cuda:1")
+    w = [W4Weight.__new__(W4Weight) for _ in range(3)]
+    for v, (K, N) in zip(w, ((64, 128), (64, 128), (128, 64))):
+        v.E, v.K, v.N, v.group, v.nbytes = 8, K, N, 32, 64
+        v.packed = Tensor((64,), torch.uint8)
+    monkeypatch.setattr(torch, "Tensor", Tensor)
+    monkeypatch.setattr(ffn, "load_library", Lib)
+    monkeypatch.setattr(ffn, "_raw_stream", lambda d: f"stream of {d}")
+    monkeypatch.setattr(layer, "moe_gate_topk", lambda *a: calls.append(("router", device[0])))
+    x = Tensor((4, 64), torch.bfloat16)
+    assert b.run(x, x, *w) is b.O
+    assert calls == [("router", 1), ("experts", 1, "stream of 1")] and device[0] == current
+    calls.clear()
+    b.route(logits_in=x)
+    assert calls == [("router", 1)]
