@@ -22,6 +22,9 @@ namespace moe {
 namespace {
 
 constexpr int64_t kMaxRow = 1 << 27;
+// Workgroups of the reduction, of 1024 threads: a launch has below 2^32 (one for each 64
+// of 2 H columns would be 2^22 of them from H = 2^27 - 31 on).
+constexpr int64_t kReduceGroups = 1 << 21;
 constexpr int kThreads = 256;  // of the kernels that share rows by waves, or re-read them
 
 template <int CTRL>
@@ -461,30 +464,33 @@ __global__ __launch_bounds__(kThreads) void ln_cols_kernel(int64_t S, int64_t H,
 }
 
 // dgamma, dbeta: the P partial sums of each of 2 H columns in a fixed order: 64
-// columns per workgroup, each of 16 waves a sixteenth of the partials, 8 loads at
-// a time. (4 waves with one load at a time took 60 us for P = 512, H = 2048: one
+// columns per workgroup at a time, each of 16 waves a sixteenth of the partials, 8 loads
+// at a time. (4 waves with one load at a time took 60 us for P = 512, H = 2048: one
 // memory latency after another.)
 __global__ __launch_bounds__(1024) void ln_reduce_kernel(int64_t P, int64_t H, const float* part,
                                                          float* dgamma, float* dbeta) {
   constexpr int W = 16, B = 8;
   __shared__ float red[W][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t j = (int64_t)blockIdx.x * 64 + lane;
-  float a = 0.f;
-  if (j < 2 * H)
-    for (int64_t p = w; p < P; p += W * B) {
-      float v[B];
+  for (int64_t j0 = (int64_t)blockIdx.x * 64; j0 < 2 * H; j0 += (int64_t)gridDim.x * 64) {
+    const int64_t j = j0 + lane;
+    float a = 0.f;
+    if (j < 2 * H)
+      for (int64_t p = w; p < P; p += W * B) {
+        float v[B];
 #pragma unroll
-      for (int e = 0; e < B; ++e) v[e] = p + e * W < P ? part[(p + e * W) * 2 * H + j] : 0.f;
+        for (int e = 0; e < B; ++e) v[e] = p + e * W < P ? part[(p + e * W) * 2 * H + j] : 0.f;
 #pragma unroll
-      for (int e = 0; e < B; ++e) a += v[e];
+        for (int e = 0; e < B; ++e) a += v[e];
+      }
+    if (j0 != (int64_t)blockIdx.x * 64) __syncthreads();  // the last columns' sums are read
+    red[w][lane] = a;
+    __syncthreads();
+    if (w == 0 && j < 2 * H) {
+#pragma unroll
+      for (int q = 1; q < W; ++q) a += red[q][lane];
+      (j < H ? dgamma[j] : dbeta[j - H]) = a;
     }
-  red[w][lane] = a;
-  __syncthreads();
-  if (w == 0 && j < 2 * H) {
-#pragma unroll
-    for (int q = 1; q < W; ++q) a += red[q][lane];
-    (j < H ? dgamma[j] : dbeta[j - H]) = a;
   }
 }
 
@@ -593,7 +599,6 @@ moe_status check_ln(int64_t S, int64_t H, int32_t dtype) {
   if (S < 0 || H < 1) return MOE_ERR_INVALID_ARGUMENT;
   if (dtype == MOE_MXFP8) return MOE_ERR_UNSUPPORTED;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARGUMENT;
-  // the column sums' launch: 32 H threads, below 2^32
   if (S >= INT32_MAX || H >= kMaxRow) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -694,8 +699,10 @@ extern "C" moe_status moe_layernorm_backward(int64_t S, int64_t H, int32_t dtype
     else
       go(bf16_t{});
   }
-  if (dgamma != nullptr)
-    ln_reduce_kernel<<<(unsigned)((2 * H + 63) / 64), 1024, 0, (hipStream_t)stream>>>(
-        S > 0 ? groups : 0, H, part, dgamma, dbeta);
+  if (dgamma != nullptr) {
+    const int64_t cols = (2 * H + 63) / 64;
+    ln_reduce_kernel<<<(unsigned)(cols < kReduceGroups ? cols : kReduceGroups), 1024, 0,
+                       (hipStream_t)stream>>>(S > 0 ? groups : 0, H, part, dgamma, dbeta);
+  }
   return enqueued();
 }

@@ -174,3 +174,21 @@ def test_gradient_against_differences():
     num = (loss(x.double(), gamma.double() + e * w) - loss(x.double(), gamma.double() - e * w)) \
         / (2 * e)
     assert abs(num - float((dg.double() * w).sum())) < 1e-4
+
+
+@pytest.mark.timeout(300)
+@pytest.mark.parametrize("H", [(1 << 27) - 1, (1 << 27) - 8])
+def test_longest_rows(H):
+    """The ends of the documented range, where one workgroup for each 64 column sums would
+    be a launch of 2^32 threads."""
+    print(f"[layernorm 1x{H}]", flush=True)
+    x, gamma, _, dy = make(1, H, BF, 7)
+    mean, rstd = torch.tensor([0.1], device=DEV), torch.tensor([0.5], device=DEV)
+    dx, dg, db = torch.empty_like(x), torch.empty(H, device=DEV), torch.empty(H, device=DEV)
+    ws = torch.empty(moe.moe_layernorm_backward_workspace_bytes(1, H), dtype=torch.uint8,
+                     device=DEV)
+    moe.moe_layernorm_backward(dy, x, gamma, mean, rstd, dx, dg, db, ws)
+    n = (x[0].double() - mean.double()) * rstd.double()
+    # one row: no sums; x - mean, its product with rstd and with dy are rounded
+    check("dgamma", dg, dy[0].double() * n, 4 * 2.0 ** -24 * (dy[0].double() * n).abs() + 1e-38)
+    assert torch.equal(db, dy[0].float())
