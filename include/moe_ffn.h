@@ -31,8 +31,8 @@ extern "C" {
  * Layer norm over rows of X [S][H]:
  *   m_s = (1/H) sum_h X_sh,  v_s = (1/H) sum_h (X_sh - m_s)^2,  r_s = 1 / sqrt(v_s + eps)
  *   Y_sh = (X_sh - m_s) r_s gamma_h + beta_h
- * dtype MOE_F32 or MOE_BF16 (X, gamma, beta, Y); statistics and sums are fp32,
- * Y is rounded once. Any S from 0 and H from 1 on, S below 2^31 - 1, H below 2^27
+ * dtype MOE_F32 or MOE_BF16 (X, gamma, beta, Y); statistics and sums are fp32
+ * (those over a row longer than 16384 compensated), Y is rounded once. Any S from 0 and H from 1 on, S below 2^31 - 1, H below 2^27
  * (else MOE_ERR_UNSUPPORTED, as for arrays off their element's alignment or a
  * workspace off 16 bytes); arrays whose rows are whole 16-byte vectors
  * and aligned to them are fastest.

@@ -192,3 +192,51 @@ def test_longest_rows(H):
     # one row: no sums; x - mean, its product with rstd and with dy are rounded
     check("dgamma", dg, dy[0].double() * n, 4 * 2.0 ** -24 * (dy[0].double() * n).abs() + 1e-38)
     assert torch.equal(db, dy[0].float())
+
+
+@pytest.mark.timeout(300)
+@pytest.mark.parametrize("H", [1 << 24, (1 << 24) + 3, 1 << 26])
+def test_long_rows_of_nearly_equal_values(H):
+    """Each of the sums over a row is within 20 roundings of its terms' magnitudes, however
+    long the row: 3 within a vector, 2 of the compensated sum over vectors, 6 within the
+    wave and 3 over the waves, 4 for the terms themselves, 2 for the division by H."""
+    print(f"[layernorm 1x{H}]", flush=True)
+    g = gen(8)
+    x = (torch.randn((1, H), generator=g, device=DEV) * 1e-3 + 0.1)
+    dy = (torch.randn((1, H), generator=g, device=DEV) * 1e-3 + 0.1)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+    moe.moe_layernorm_forward(x, None, None, 1e-9, y, mean, rstd)
+    u, k = 2.0 ** -24, 20
+    x64 = x.double()
+    m = x64.mean()
+    v = (x64 - m).square().mean()
+    r = 1 / torch.sqrt(v + 1e-9)
+    em = k * u * x64.abs().mean()
+    er = r * (0.5 * (k * u * v + em * em) / (v + 1e-9) + 4 * u)  # cf. ln_ref
+    check("mean", mean, m[None], em[None])
+    check("rstd", rstd, r[None], er[None])
+    n = (x64 - m) * r
+    check("y", y, n, r * em + n.abs() * (er / r + 5 * u))
+    moe.moe_layernorm_backward(dy, x, None, mean, rstd, dx, None, None, None)
+    n = (x64 - mean.double()) * rstd.double()
+    d = dy.double()
+    c0, c1 = d.mean(), (d * n).mean()
+    e0, e1 = k * u * d.abs().mean(), k * u * (d * n).abs().mean()
+    check("dx", dx, rstd.double() * (d - c0 - n * c1),
+          rstd.double() * (e0 + n.abs() * e1 + 6 * u * (d.abs() + c0.abs() + (n * c1).abs())))
+
+
+def test_long_rows_that_are_not_finite():
+    """A sum that leaves fp32's range, and infinities and NaN, as in shorter rows."""
+    H = 20008
+    x = torch.ones((5, H), device=DEV)
+    x[1, 7], x[2, 9], x[3, 11] = float("inf"), float("-inf"), float("nan")
+    x[4] = 3e38
+    y = torch.empty_like(x)
+    mean, rstd = torch.empty(5, device=DEV), torch.empty(5, device=DEV)
+    moe.moe_layernorm_forward(x, None, None, 1e-5, y, mean, rstd)
+    inf = float("inf")
+    assert mean[:3].tolist() == [1.0, inf, -inf] and bool(torch.isnan(mean[3]))
+    assert float(mean[4]) == inf and bool((y[0] == 0).all())
+    assert bool(torch.isnan(y[1, 7])) and bool(torch.isnan(y[3]).all())
