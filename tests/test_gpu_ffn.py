@@ -285,3 +285,18 @@ def test_binding_refusals():
         moe.moe_ffn_forward(b.shape, x, wu, wg, wd, None, None, b.O, b.ws[:64])
     with pytest.raises(moe.MoeError, match="INVALID"):
         moe.moe_ffn_forward(b.shape, x, wu, wg, wd, b.U, None, b.O, b.ws)
+
+
+# What SHAPES and TILES leave out of the plan's choices: dh, down and both weight
+# gradients on the 256 x 256 tile with splits of K, down, dh and dW_down on 128 x 128 with
+# splits, down on 256 x 128 with splits, up in one split over 64 rows; fp32: down and dX on
+# 128 x 128 without splits, up, dh, down and dX over several row tiles of 16 with splits.
+MORE_TILES = [(17, 1032, 72), (33, 136, 7176), (65, 4104, 4104), (257, 7176, 4104),
+              (4100, 4104, 72), (6000, 264, 7176), (8200, 7176, 136)]
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("S,H,D", MORE_TILES)
+def test_remaining_tiles(S, H, D, t):
+    test_forward(S, H, D, t)
+    test_backward(S, H, D, t)
