@@ -300,3 +300,61 @@ MORE_TILES = [(17, 1032, 72), (33, 136, 7176), (65, 4104, 4104), (257, 7176, 410
 def test_remaining_tiles(S, H, D, t):
     test_forward(S, H, D, t)
     test_backward(S, H, D, t)
+
+
+@pytest.mark.timeout(300)
+def test_every_weight_gradient_past_4_gib():
+    """dO is zero but in 8 early rows and the 4157 whose U, G, dU, dG and h lie past 4 GiB,
+    so that each weight gradient is the sum of those rows' products, within the usual
+    bound of that many terms; without the rows past 4 GiB it would miss it."""
+    S, H, D = (1 << 20) + 77, 8, 2056
+    print(f"[ffn {S}x{H}x{D}]", flush=True)
+    x, wu, wg, wd, do = make(S, H, D, BF, 16)
+    past = -(-(1 << 32) // (D * 2))
+    do[8:past] = 0
+    live = torch.cat([torch.arange(8), torch.arange(past, S)]).to(DEV)
+    assert past == 1044496 and live.numel() == 8 + S - past
+    b = FFNBuffers(S, H, D, train=True, out_f32=True, device=DEV)
+    b.forward(x, wu, wg, wd)
+    b.ws.fill_(0xFF)
+    got = b.backward(do, x, wu, wg, wd)
+    refs, errs = ffn_bwd_ref(do[live], x[live], wu, wg, wd, b.U[live], b.G[live], True)
+    early = ffn_bwd_ref(do[:8], x[:8], wu, wg, wd, b.U[:8], b.G[:8], True)[0]
+    check("dx", got[0][live], refs[0], rounded(refs[0], errs[0], BF))
+    assert not bool(got[0][8:past].any())
+    for n, v, r, e, q in zip(("dwu", "dwg", "dwd"), got[1:], refs[1:], errs[1:], early[1:]):
+        bound = rounded(r, e, F32)
+        check(n, v, r, bound)
+        assert float(((r - q).abs() > bound).double().mean()) > 0.9, n  # the bound says something
+
+
+@pytest.mark.timeout(300)
+def test_weights_past_4_gib():
+    """Each weight and its gradient exceed 4 GiB: the first and the last 300 rows and
+    columns. Small integers, and pre-activations of 32, where SiLU is the identity in fp32
+    and its derivative 1, so that every sum stays an integer below 2^24 and exact."""
+    S, H, D = 17, 32776, 32776
+    print(f"[ffn {S}x{H}x{D}]", flush=True)
+    g = gen(17)
+    ints = lambda *n: torch.randint(-1, 2, n, generator=g, device=DEV, dtype=torch.int8).float()
+    x, wu, wg, wd, do = ints(S, H), ints(H, D), ints(H, D), ints(D, H), ints(S, H)
+    assert wu.numel() * 4 > 1 << 32
+    b = FFNBuffers(S, H, D, moe.MOE_F32, train=True, device=DEV)
+    b.forward(x, wu, wg, wd)
+    ends = torch.cat([torch.arange(300), torch.arange(D - 300, D)]).to(DEV)
+    assert torch.equal(b.U[:, ends].double(), mm(x, wu[:, ends]))
+    assert torch.equal(b.G[:, ends].double(), mm(x, wg[:, ends]))
+    u, gg = torch.full((S, D), 32.0, device=DEV), ints(S, D)
+    dx, dwu, dwg, dwd = b.backward(do, x, wu, wg, wd, u, gg)
+    dh = torch.cat([mm(do, p.t()) for p in wd.split(4096)], 1)
+    du, dg = dh * gg.double(), dh * 32
+    assert torch.equal(dx[:, ends].double(), mm(du, wu[ends].t()) + mm(dg, wg[ends].t()))
+    xt, ht = x.t().contiguous(), (gg * 32).t().contiguous()
+    for v, a, c in ((dwu, xt, du), (dwg, xt, dg), (dwd, ht, do)):
+        assert torch.equal(v[ends].double(), mm(a[ends], c))
+        assert torch.equal(v[:, ends].double(), mm(a, c[:, ends]))
+    # the second product of the forward pass: its last columns from the kept U and G
+    h = b.U.double() * torch.sigmoid(b.U.double()) * b.G.double()
+    o, m = mm(h, wd[:, ends]), mm(h.abs(), wd[:, ends].abs())
+    check("o", b.O[:, ends], o, (D + 8 * 600) * 2.0 ** -24 * m)  # |U| stays below 600
+    assert float(b.U.abs().max()) < 600
