@@ -3,6 +3,7 @@ arguments on the host (no GPU: each call returns before anything is enqueued).""
 import ctypes
 import os
 import re
+import shutil
 import subprocess
 
 import pytest
@@ -404,3 +405,29 @@ def test_router_and_experts_run_on_the_buffers_device(lib, monkeypatch, current)
     calls.clear()
     b.route(logits_in=x)
     assert calls == [("router", 1)]
+
+
+def test_layer_digest_follows_the_layers_code_only(tmp_path, monkeypatch):
+    """On a copy of the sources: code of the operators in csrc/ffn/ and of moe_ffn.h does not
+    change the digest that the layer's counter records carry, the layer's own does."""
+    pkg = tmp_path / os.path.basename(buildlib.PKG)
+    shutil.copytree(os.path.join(buildlib.PKG, "csrc"), pkg / "csrc")
+    shutil.copytree(os.path.join(ROOT, "include"), tmp_path / "include")
+    before = buildlib.source_digest()
+    monkeypatch.setattr(buildlib, "PKG", str(pkg))
+    monkeypatch.setattr(buildlib, "ROOT", str(tmp_path))
+    assert buildlib.source_digest() == before
+
+    def edit(path):
+        path.write_text(path.read_text() + "\nint added;\n")
+        return buildlib.source_digest()
+
+    mine = sorted((pkg / "csrc" / "ffn").iterdir())
+    assert any(f.name == "w4.hip" for f in mine)
+    for f in (*mine, tmp_path / "include" / "moe_ffn.h"):
+        assert edit(f) == before, f.name
+    for f in (*sorted(f for f in (pkg / "csrc").iterdir() if f.is_file()),
+              tmp_path / "include" / "moe.h"):
+        after = edit(f)
+        assert after != before, f.name
+        before = after
