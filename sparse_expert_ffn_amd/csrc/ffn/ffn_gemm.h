@@ -85,6 +85,7 @@ struct Operand {
   static constexpr int ROWB = PW * ES;         // MC: bytes per K row of a panel
   static constexpr int CPU = ES;               // MC: 16-byte chunks per 16-column unit
   static_assert(KC || ROWB == 128 || ROWB == 256, "panel width");
+  static_assert(!KC || BASES == 1, "two bases: a DUAL product's B, K outermost");
   static_assert(INSTR % NW == 0 || INSTR < NW, "loads split evenly");
 
   int wave;
@@ -116,9 +117,8 @@ struct Operand {
         const int r = q * 8 + (lane >> 3);
         // the chunk is the same for every t (rows 8 NW apart, or one load only)
         const int c = (lane & 7) ^ swz_kc(r);
-        const int rr = BASES == 2 ? r % PW : r;
         chunk_k = c * (16 / ES);
-        off[t] = r0 + rr < n ? (uint32_t)(rr * ld * ES + c * 16) : kOutOfRange;
+        off[t] = r0 + r < n ? (uint32_t)(r * ld * ES + c * 16) : kOutOfRange;
       } else {
         constexpr int CH = ROWB / 16;  // chunks per K row
         const int kr = (q % PANEL_INSTR) * (64 / CH) + lane / CH;

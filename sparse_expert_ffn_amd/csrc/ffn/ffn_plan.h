@@ -123,7 +123,7 @@ void launch_gemm(const GemmPlan& p, const GemmArgs& g, const EP& ep, hipStream_t
       launch_tile<TileCore<T, 128, 128, 2, DUAL, AKC, BKC, 2, 4, 2>>(g, ep, st);
       return;
     }
-    if constexpr (AKC)
+    if constexpr (AKC) {
       if (p.tile == 2) {
         if (p.tiles_m == 1)
           launch_tile<TileCore<T, 16, 64, NP, DUAL, AKC, BKC, 1, 2, 3, true>>(g, ep, st);
@@ -131,7 +131,8 @@ void launch_gemm(const GemmPlan& p, const GemmArgs& g, const EP& ep, hipStream_t
           launch_tile<TileCore<T, 16, 64, NP, DUAL, AKC, BKC, 1, 2, 3>>(g, ep, st);
         return;
       }
-      launch_tile<TileCore<T, 64, 64, NP, DUAL, AKC, BKC, 2, 2, 2>>(g, ep, st);
+    }
+    launch_tile<TileCore<T, 64, 64, NP, DUAL, AKC, BKC, 2, 2, 2>>(g, ep, st);
   } else {
     if (p.tile == 0)
       launch_tile<TileCore<T, 256, 256, 2, DUAL, AKC, BKC, 2, 4, 2>>(g, ep, st);

@@ -710,7 +710,7 @@ extern "C" moe_status moe_layernorm_backward(int64_t S, int64_t H, int32_t dtype
   if (S > 0) {
     auto go = [&](auto tag) {
       using T = decltype(tag);
-        auto call = [&](auto rag) {
+      auto call = [&](auto rag) {
         backward_t<T, decltype(rag)::value>(p, S, H, (const T*)dY, (const T*)X, (const T*)gamma,
                                             mean, rstd, (T*)dX, part, groups,
                                             (hipStream_t)stream);
