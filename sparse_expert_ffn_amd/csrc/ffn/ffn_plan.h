@@ -45,7 +45,9 @@ struct GemmPlan {
 
 // The tile and the splits with the least estimated time: the workgroups of a CU, as
 // many at once as it holds, plus the splits' sums' way through memory and the
-// launch that joins them.
+// launch that joins them. The stages' times are of operands in the caches: weights that
+// come from HBM take longer than it expects (64 x 7168 x 2048 bf16: 9 and 7 us expected,
+// 17 and 13 taken).
 // `tiles`: bit mask of the tiles that the product has kernels for.
 inline GemmPlan plan_gemm(bool f32, unsigned tiles, bool dual, int64_t M, int64_t N, int64_t K,
                           int pairs) {
@@ -156,7 +158,10 @@ void launch_gemm(const GemmPlan& p, const GemmArgs& g, const EP& ep, hipStream_t
 // ------------------------------------------------------------ epilogues
 struct NoPre {};
 
-// h = SiLU(u) g from the fp32 sums; u and g kept for a backward pass.
+// h = SiLU(u) g from the fp32 sums; u and g kept for a backward pass. In bf16 h is rounded
+// to the next product's operand, as the MoE layer's is: the outputs' error against 64 bits
+// (2-norm) is 0.0023 so, 0.0017 from their own rounding alone. Kept in two bf16 parts it
+// would take a third more MFMAs in the pass, which is bound by them for many tokens.
 template <typename T>
 struct EpSwiglu {
   T *h, *U, *G;
@@ -196,7 +201,8 @@ struct EpStore {
   }
 };
 // From dh: dU, dG, and h again (all operands of the products that follow); h may
-// be null (frozen weights).
+// be null (frozen weights). In bf16 they are rounded as such: 0.0023 instead of 0.0017 in
+// each gradient; in two parts each the pass would take 22 / 12 of its MFMAs.
 template <typename T>
 struct EpSwigluBwd {
   const T *U, *G;

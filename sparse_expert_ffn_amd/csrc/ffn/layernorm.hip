@@ -92,7 +92,8 @@ struct LongSum {
 // element: 700 x 9001 fp32 forward 40 -> 15 us, 20000 x 511 bf16 21 -> 10 us).
 // Rows are read and written once. Aligned ones both with the non-temporal hint (16384 x
 // 7168 bf16, cold caches: forward 119 -> 88 us, backward 169 -> 131 us, 5.4 TB/s; the
-// hint on the stores alone made them slower). The others' vectors share cache lines with
+// hint on the stores alone made them slower): arrays about as large as the caches, the norm
+// alone; what the hint costs whoever reads a small Y next was not timed. The others' vectors share cache lines with
 // their neighbours: the hint on the stores only (30000 x 511 bf16 backward: none 28 us,
 // stores 24, both 28; 16384 x 7167 forward: 106, 78, 103).
 template <typename T>
@@ -551,7 +552,8 @@ LnPlan ln_plan(int64_t H, int es, bool aligned) {
 // Workgroups of the backward pass, each with partial sums of its own, which go through
 // memory twice: at most 512 (1024: dX as fast, the sums' way twice as long), and with
 // fewer than 2048 rows one for 4 rows, but 128 at least (500 x 4096 bf16: 512 workgroups
-// 13.9 us, 128 11.2; 1000 x 8192 fp32: 32.5 and, with 250, 26.2).
+// 13.9 us, 128 11.2; 1000 x 8192 fp32: 32.5 and, with 250, 26.2). The rows' length is not
+// weighed: 512 x 16384 fp32 takes 128, half of the CUs, and 39 us, where its bytes take 20.
 constexpr int64_t kBwdGroups = 512;
 constexpr int64_t kRowGroups = 2048;  // of the forward pass: 8 of 256 threads to a CU
 

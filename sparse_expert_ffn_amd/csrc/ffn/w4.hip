@@ -45,6 +45,8 @@ __host__ __device__ inline int64_t tiles_n(int64_t N) { return (N + kTileN - 1) 
 
 bool group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
 
+// One thread per column and group, which it reads twice (256 x 2048 x 768 bf16, groups of
+// 64: 780 us, 1.6 TB/s; once per weight).
 template <typename T>
 __global__ void w4_quantize_kernel(const T* W, int64_t E, int64_t K, int64_t N, int group,
                                    uint8_t* codes, bf16_t* scales) {
@@ -67,7 +69,8 @@ __global__ void w4_quantize_kernel(const T* W, int64_t E, int64_t K, int64_t N, 
 }
 
 // One workgroup: 128 rows by 128 columns (8 tiles) of codes through LDS, so that they
-// are read as 128 consecutive bytes and written as tiles.
+// are read as 128 consecutive bytes and written as tiles (256 x 2048 x 768, groups of 64:
+// 138 us, 4.6 TB/s).
 __global__ __launch_bounds__(256) void w4_pack_kernel(const uint8_t* codes, const bf16_t* scales,
                                                       int64_t K, int64_t N, int group,
                                                       char* packed, int64_t blocks) {
@@ -216,6 +219,9 @@ struct Step {
   }
 };
 
+// (Rows with a matrix each, 2048 x 768, 64 matrices, groups of 64: 8 rows 7.3 us; 64 rows
+// of 39 matrices 15 us, 2.2 TB/s; 512 rows, 16 of a matrix at a time, 50 us.)
+//
 // The rows of the workgroup's list (f indexes) that blockIdx's entry stands for:
 //   by_row: entry y stands for ids[y]'s expert if no earlier row has it;
 //   else:   entry y stands for expert y.
@@ -247,6 +253,9 @@ constexpr int tiles_per_wave(int op) { return op == kDown ? 2 : 1; }
 // (3 waves) 86 and 57 us; 4 steps 94 and 78 us.
 constexpr int steps_ahead(int op) { return op == kMatvec ? 2 : 1; }
 
+// h is rounded to bf16, the down product's operand, as the MoE layer's is (64 tokens of
+// 2048 x 768: 0.0022 in the outputs, 2-norm against 64 bits, 0.0017 from their own
+// rounding alone).
 template <int OP>
 __device__ __forceinline__ void w4_store(void* out, int64_t o, float v, float v1, int out_f32) {
   if constexpr (OP == kUpgate)
