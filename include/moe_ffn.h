@@ -1,7 +1,8 @@
 /*
  * sparse_expert_ffn_amd — C ABI of the operators around the MoE layer on one
  * MI355X (gfx950) GPU: layer norm, the dense gated feed-forward block with its
- * backward pass, and products with 4-bit weights for decode.
+ * backward pass, products with 4-bit weights for decode, and products in 8-bit
+ * integers.
  *
  * The conventions are those of moe.h: device pointers to dense row-major
  * arrays, every call validates on the host, enqueues kernels on `stream` (of
@@ -177,6 +178,65 @@ moe_status moe_w4_forward(const moe_shape* shape, int32_t group, const void* A,
                           const void* Ws_up, const void* Ws_gate, const void* Ws_down,
                           const int32_t* topk_ids, const float* topk_weights, void* O,
                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * 8-bit integers with a scale for each token and channel. A weight matrix W [K][N] is
+ * held as codes -127..127 and one fp32 scale per column, W_kn = code_kn scale_n; a row
+ * of activations as codes and one scale. A vector x (a column of W, a row of X) has
+ *   scale = max |x| / 127 rounded to fp32,  code = x / scale rounded to the nearest
+ *   integer, ties to even (0 where the scale is 0, clamped to [-127, 127])
+ * decided exactly. A vector that holds an infinity or NaN gets a scale of NaN and
+ * codes 0: every product with it is NaN.
+ *
+ * moe_quantize_i8 gives the codes [E][K][N] and scales [E][N] of a bf16 or fp32
+ * tensor W [E][K][N]. moe_pack_i8_weights lays codes and scales, of whatever
+ * quantiser (codes of -128 are allowed), out for the products below:
+ * moe_i8_weight_bytes(E, K, N) bytes at `packed`. Layout, matrix by matrix: tiles of
+ * 16 columns n by 64 rows k, column tile by column tile, k ascending, 1024 bytes each:
+ * 16 bytes for each lane l = 16 q + c, rows 16 q .. + 15 of column c; then the scales,
+ * one for each column of the tiles. What fills up a tile is 0. Both calls are one-time
+ * steps, at weight load. moe_quantize_i8_rows gives the codes [S][K] and scales [S] of
+ * the rows of X [S][K].
+ *
+ * K a multiple of 16 up to 131072 (sums of products of codes stay exact in 32 bits;
+ * for codes of -128 on both sides below that), N a multiple of 8 below 2^22, 16-byte
+ * aligned arrays (scales: 4), else MOE_ERR_UNSUPPORTED.
+ */
+size_t moe_i8_weight_bytes(int64_t E, int64_t K, int64_t N); /* 0 if unsupported */
+moe_status moe_quantize_i8(const void* W, int64_t E, int64_t K, int64_t N, int32_t dtype,
+                           int8_t* codes, float* scales, void* stream);
+moe_status moe_pack_i8_weights(const int8_t* codes, const float* scales, int64_t E, int64_t K,
+                               int64_t N, void* packed, void* stream);
+moe_status moe_quantize_i8_rows(const void* X, int64_t S, int64_t K, int32_t dtype,
+                                int8_t* codes, float* scales, void* stream);
+
+/*
+ * Y = X W in that arithmetic: Y_sn = (sum_k xcode_sk wcode_kn) xscale_s wscale_n, the
+ * sum exact in integers, scaled in fp32, rounded once. Any S: one token to a prompt.
+ *   row_scales  NULL: X is [S][K] of `dtype` (MOE_F32 or MOE_BF16), quantised by the
+ *               call as moe_quantize_i8_rows does.
+ *               [S] fp32: X holds [S][K] codes (int8) with these scales
+ *   W           packed with E = 1;  Y [S][N] of `dtype`, fp32 with flags = MOE_OUTPUT_F32
+ * A NaN or infinity in a row of X gives a row of NaN.
+ */
+size_t moe_i8_matmul_workspace_bytes(int64_t S, int64_t K, int64_t N); /* 0 if unsupported */
+moe_status moe_i8_matmul(int64_t S, int64_t K, int64_t N, int32_t dtype, int32_t flags,
+                         const void* X, const float* row_scales, const void* W, void* Y,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The dense gated feed-forward block (moe_ffn_forward's) in that arithmetic:
+ *   U = X W_up,  G = X W_gate,  h = SiLU(U) * G,  O = h W_down,
+ * each product as in moe_i8_matmul: the rows of X and those of h (kept in fp32, not
+ * rounded before) are quantised.
+ *   X [S][H] dtype;  W_up, W_gate packed [H][D], W_down packed [D][H];  O [S][H] dtype, or
+ *   fp32 with MOE_OUTPUT_F32
+ * H and D multiples of 16 up to 131072.
+ */
+size_t moe_i8_ffn_workspace_bytes(const moe_ffn_shape* shape); /* 0 if unsupported */
+moe_status moe_i8_ffn_forward(const moe_ffn_shape* shape, const void* X, const void* W_up,
+                              const void* W_gate, const void* W_down, void* O, void* workspace,
+                              size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

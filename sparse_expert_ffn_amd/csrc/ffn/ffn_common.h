@@ -79,4 +79,12 @@ __device__ __forceinline__ void store_n(bf16_t* p, const float (&v)[W]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
+// W sums of 8-bit codes, as they are.
+template <int W>
+__device__ __forceinline__ void store_n(int* p, const int (&v)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; i += 4)
+    *reinterpret_cast<int4*>(p + i) = make_int4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+
 }  // namespace moe

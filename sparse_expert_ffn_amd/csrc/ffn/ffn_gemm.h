@@ -4,12 +4,14 @@
 //
 //   KC operand: rows of K contiguous values (A [M][K], B [N][K])
 //   MC operand: K rows of contiguous values (A [K][M], B [K][N])
+//   packed operand (8-bit integers): B in tiles of 16 columns x 64 K values, in the
+//   order in which the MFMA takes them
 //
 // C may have two panels of columns with a B of their own (DUAL: up and gate, or
 // their gradients), and K may run over two pairs of operands in turn (dX = dU
 // W_up^T + dG W_gate^T).
 //
-// K stages of 128 bytes (64 bf16, 32 fp32) go from global memory straight into a
+// K stages of 128 bytes (64 bf16, 32 fp32, 128 int8) go from global memory straight into a
 // ring of LDS slots (16 bytes per lane). KC operands lie there as rows of 128
 // bytes and are read 16 bytes per lane, MC operands as K rows of a panel of up to
 // 256 bytes and are read transposed (bf16: ds_read_b64_tr_b16; fp32: 4 bytes per
@@ -17,7 +19,8 @@
 // bank conflicts (fp32 MC: 64-byte units ordered by the lane group).
 //   bf16: v_mfma_f32_16x16x32_bf16, a lane's 16 bytes are 8 K values of a row;
 //   fp32: four v_mfma_f32_16x16x4_f32, a lane's 16 bytes are 4 K values, one per
-//         MFMA: any order of K serves that is the same for both operands.
+//         MFMA: any order of K serves that is the same for both operands;
+//   int8: v_mfma_i32_16x16x64_i8, a lane's 16 bytes are 16 K values of a row.
 // The MFMA takes B's fragment as its first operand, so a lane ends up with 4
 // consecutive columns of one row and loads and stores them as one access.
 //
@@ -53,7 +56,7 @@ struct GemmArgs {
   int split_stages;       // K stages per split
   int splits;
   int tiles_m, tiles_n;
-  float* part;            // splits > 1: [splits][panels][M][N]
+  float* part;            // splits > 1: [splits][panels][M][N] (int32 sums of 8-bit codes)
 };
 
 constexpr uint32_t kOutOfRange = 0x80000000u;  // above every record count used here
@@ -201,6 +204,73 @@ struct Operand {
   }
 };
 
+// B of a product in 8-bit integers, packed: tiles of 16 columns x 64 K values of 1 KB,
+// column tile by column tile, K ascending; 16 bytes for each lane l: column l % 16, K
+// values 16 (l / 16) .. + 15. A K stage is two tiles of each column tile; they lie in LDS
+// as in memory, and a fragment read is 1 KB in lane order: no chunk order is needed.
+// What a stage reads behind the last K tile (the next column tile's codes) meets zeros of
+// A; column tiles that are not there read as zeros. ld: K tiles of a column tile.
+template <int R, int PW, int BASES, int NW, bool ONCE>
+struct PackedOperand {
+  static constexpr int BYTES = R * 128;
+  static constexpr int INSTR = BYTES / 1024;
+  static constexpr int PER_WAVE = (INSTR + NW - 1) / NW;
+  static constexpr int PANEL_INSTR = PW / 8;
+  static_assert(INSTR % NW == 0 || INSTR < NW, "loads split evenly");
+
+  int wave;
+  uint32_t off[PER_WAVE];
+  uint64_t base[BASES];
+  int64_t left[BASES];
+  i32x4_t srd[BASES];
+  uint32_t rd;
+
+  __device__ __forceinline__ void setup(int wave_, int64_t ld, int64_t n0, int64_t n, int w0) {
+    const int lane = threadIdx.x & 63;
+    wave = wave_;
+#pragma unroll
+    for (int t = 0; t < PER_WAVE; ++t) {
+      const int q = wave + NW * t;
+      const int c = (BASES == 2 ? q % PANEL_INSTR : q) / 2;  // column tile
+      off[t] = n0 + 16 * c < n ? (uint32_t)((c * ld + (q & 1)) * 1024 + lane * 16) : kOutOfRange;
+    }
+    rd = (uint32_t)(w0 / 16 * 2048 + lane * 16);
+  }
+  __device__ __forceinline__ void seek(int b, const void* p, int64_t ld, int64_t n0, int64_t n,
+                                       int64_t, int64_t k0) {
+    const int64_t at = (n0 / 16 * ld + k0 / 64) * 1024;
+    base[b] = reinterpret_cast<uint64_t>(p) + (uint64_t)at;
+    left[b] = (n + 15) / 16 * ld * 1024 - at;
+    srd[b] = window_srd(base[b], left[b]);
+  }
+  __device__ __forceinline__ void advance() {
+#pragma unroll
+    for (int b = 0; b < BASES; ++b) {
+      base[b] += 2048;
+      left[b] -= 2048;
+      srd[b] = window_srd(base[b], left[b]);
+    }
+  }
+  __device__ __forceinline__ void close() {
+#pragma unroll
+    for (int b = 0; b < BASES; ++b) {
+      left[b] = 0;
+      srd[b].z = 0;
+    }
+  }
+  __device__ __forceinline__ void issue(char* lds, int t, int) const {
+    const int q = wave + NW * t;
+    if (INSTR % NW != 0 && q >= INSTR) return;
+    int b = 0;
+    if constexpr (BASES == 2) b = PANEL_INSTR % NW == 0 ? NW * t / PANEL_INSTR : q / PANEL_INSTR;
+    const i32x4_t r = b == 0 ? srd[0] : srd[BASES - 1];
+    dma16<false, ONCE>(r, off[t], lds + q * 1024);
+  }
+  __device__ __forceinline__ uint4 frag(const char* lds, int p, int j, int ks) const {
+    return *reinterpret_cast<const uint4*>(lds + rd + (p * PW / 8 + 2 * j + ks) * 1024);
+  }
+};
+
 // BM x BN tile by WM x WN waves, NP column panels of BN / NP, DUAL: each panel
 // has a B and a C of its own. A wave covers the same BN / NP / WN columns of each
 // panel. NST: LDS slots.
@@ -217,7 +287,11 @@ struct TileCore {
   static constexpr int PMAX = 256 / (int)sizeof(T);
   static constexpr int PWA = AKC ? BM : (BM < PMAX ? BM : PMAX);
   using OpA = Operand<T, AKC, BM, PWA, 1, NW, false>;
-  using OpB = Operand<T, BKC, BN, PWB, DUAL ? 2 : 1, NW, ONCE>;
+  static constexpr bool I8 = sizeof(T) == 1;
+  using OpB = std::conditional_t<I8, PackedOperand<BN, PWB, DUAL ? 2 : 1, NW, ONCE>,
+                                 Operand<T, BKC, BN, PWB, DUAL ? 2 : 1, NW, ONCE>>;
+  using Val = std::conditional_t<I8, int, float>;       // of a sum
+  using Acc = std::conditional_t<I8, i32x4_t, f32x4_t>;
   static constexpr int MI = BM / WM / 16;
   static constexpr int NIP = PWB / WN / 16;  // 16-column blocks per wave and panel
   static constexpr int NI = NP * NIP;
@@ -227,10 +301,11 @@ struct TileCore {
   static constexpr int PIECES = OpA::PER_WAVE + OpB::PER_WAVE;
   static_assert(MI >= 1 && NIP >= 1, "tile too small for the waves");
   static_assert(AKC || (PWA % (BM / WM) == 0 && (MI & (MI - 1)) == 0), "A blocks in one panel");
-  static_assert(BKC || (NIP & (NIP - 1)) == 0, "B blocks");
+  static_assert(I8 || BKC || (NIP & (NIP - 1)) == 0, "B blocks");
+  static_assert(!I8 || AKC, "codes of rows");
   static_assert((NST - 1) * PIECES < 64, "vmcnt range");
 
-  f32x4_t acc[MI][NI];
+  Acc acc[MI][NI];
   OpA a;
   OpB b;
   // Where an operand's next stage to load lies: its pair, the pair's K values from
@@ -296,7 +371,11 @@ struct TileCore {
       for (int e = 0; e < (sizeof(T) == 4 ? 4 : 1); ++e)
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
-          if constexpr (sizeof(T) == 4)
+          if constexpr (I8)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                __builtin_bit_cast(i32x4_t, fb[cur][j]),
+                __builtin_bit_cast(i32x4_t, fa[cur][i]), acc[i][j], 0, 0, 0);
+          else if constexpr (sizeof(T) == 4)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
                 __builtin_bit_cast(f32x4_t, fb[cur][j])[e],
                 __builtin_bit_cast(f32x4_t, fa[cur][i])[e], acc[i][j], 0, 0, 0);
@@ -339,7 +418,7 @@ struct TileCore {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NI; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < NI; ++j) acc[i][j] = Acc{};
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     a.setup(wave, g.lda, m0, g.M, wave / WN * (BM / WM));
     b.setup(wave, g.ldb, n0, g.N, wave % WN * (PWB / WN));
@@ -435,9 +514,9 @@ struct TileCore {
   }
 
   // Consecutive columns of one row that a lane handles in the epilogue: the MFMA
-  // leaves 4; in bf16 two neighbouring blocks swap lane rows to make it 8, one
+  // leaves 4; but in fp32 two neighbouring blocks swap lane rows to make it 8, one
   // 16-byte access.
-  static constexpr int W = sizeof(T) == 2 && NIP % 2 == 0 ? 8 : 4;
+  static constexpr int W = sizeof(T) <= 2 && NIP % 2 == 0 ? 8 : 4;
   static constexpr int BPG = W / 4;            // blocks per group of W columns
   static constexpr int GROUPS = (DUAL ? NIP : NI) / BPG;  // per row block
 
@@ -452,7 +531,7 @@ struct TileCore {
     return W == 8 ? c + (lg & 1) * 16 + (lg >> 1) * 8 : c + lg * 4;
   }
   // Its values (of panel 1 with p = 1 in a DUAL tile).
-  __device__ __forceinline__ void group_values(int i, int q, int p, float (&v)[W]) {
+  __device__ __forceinline__ void group_values(int i, int q, int p, Val (&v)[W]) {
     const int j = p * NIP + q * BPG;
     if constexpr (W == 8) {
       // lane rows 0..3 hold columns 0, 4, 8, 12 and up of both blocks; after odd rows of
@@ -461,11 +540,13 @@ struct TileCore {
       // second's
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][r]),
-                                                        __float_as_uint(acc[i][j + 1][r]),
+        const Val a = acc[i][j][r], b = acc[i][j + 1][r];
+        const auto w = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a),
+                                                        __builtin_bit_cast(uint32_t, b),
                                                         false, false);
-        v[r] = __uint_as_float(w[0]);
-        v[4 + r] = __uint_as_float(w[1]);
+        const uint32_t w0 = w[0], w1 = w[1];
+        v[r] = __builtin_bit_cast(Val, w0);
+        v[4 + r] = __builtin_bit_cast(Val, w1);
       }
     } else {
 #pragma unroll
@@ -510,8 +591,9 @@ __global__ __launch_bounds__(Core::THREADS) void gemm_kernel(GemmArgs g, EP ep) 
   Core core;
   core.run(g, gemm_lds, m0, n0, s0, ns);
   constexpr int W = Core::W, Q = Core::GROUPS;
+  using Val = typename Core::Val;
   using Pre = typename EP::template Pre<W>;
-  float* p0 = g.part + (int64_t)split * (Core::DUAL ? 2 : 1) * g.M * g.N;
+  Val* p0 = reinterpret_cast<Val*>(g.part) + (int64_t)split * (Core::DUAL ? 2 : 1) * g.M * g.N;
   const bool direct = g.splits == 1;
   Pre pre[2][Q];
   auto fetch = [&](int i) {
@@ -529,7 +611,7 @@ __global__ __launch_bounds__(Core::THREADS) void gemm_kernel(GemmArgs g, EP ep) 
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int64_t m = m0 + core.group_row(i), n = n0 + core.group_col(q);
-      float v0[W], v1[W];
+      Val v0[W], v1[W];
       core.group_values(i, q, 0, v0);
       if constexpr (Core::DUAL) core.group_values(i, q, 1, v1);
       if (m >= g.M || n >= g.N) continue;
@@ -547,7 +629,7 @@ __global__ __launch_bounds__(Core::THREADS) void gemm_kernel(GemmArgs g, EP ep) 
 }
 
 // Adds the splits' sums in split order and applies the epilogue.
-template <bool DUAL, typename EP>
+template <bool DUAL, typename Val, typename EP>
 __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs g, EP ep) {
   const int64_t per = (g.N + 3) / 4;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < g.M * per;
@@ -556,18 +638,20 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs g, EP ep) {
     typename EP::template Pre<4> pre;
     ep.pre(m, n, pre);
     constexpr int P = DUAL ? 2 : 1;
-    float v[2][4] = {};
-    const float* q = g.part + m * g.N + n;
+    using V4 = std::conditional_t<std::is_same_v<Val, int>, i32x4_t, f32x4_t>;
+    Val v[2][4] = {};
+    const Val* q = reinterpret_cast<const Val*>(g.part) + m * g.N + n;
     const int64_t panel = g.M * g.N;
     // 8 splits' loads in flight; the sums are added in split order
     for (int s = 0; s < g.splits; s += 8) {
-      f32x4_t w[8][P];
+      V4 w[8][P];
 #pragma unroll
       for (int e = 0; e < 8; ++e)
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          w[e][p] = s + e < g.splits ? load4(q + ((s + e) * P + p) * panel)
-                                     : f32x4_t{0.f, 0.f, 0.f, 0.f};
+          w[e][p] = s + e < g.splits
+                        ? *reinterpret_cast<const V4*>(q + ((s + e) * P + p) * panel)
+                        : V4{};
 #pragma unroll
       for (int e = 0; e < 8; ++e)
 #pragma unroll

@@ -31,6 +31,13 @@ constexpr TileCost kF32Tiles[] = {
     {64, 64, 32, 5, 300.f, 510.f, 2000.f},
     {16, 64, 32, 5, 250.f, 350.f, 2300.f},
 };
+constexpr TileCost kI8Tiles[] = {
+    {256, 256, 128, 1, 0.f, 1560.f, 6000.f},
+    {128, 128, 128, 2, 280.f, 440.f, 4000.f},
+    {64, 128, 128, 2, 50.f, 370.f, 3500.f},
+    {16, 128, 128, 2, 150.f, 250.f, 3000.f},
+    {256, 128, 128, 1, 0.f, 950.f, 4500.f},
+};
 constexpr int kCus = 256;
 // Workgroups of a launch: with up to 512 threads each, below 2^32 threads. The largest
 // tile stays below it for every shape that check_ffn lets through.
@@ -48,15 +55,19 @@ struct GemmPlan {
 // launch that joins them. The stages' times are of operands in the caches: weights that
 // come from HBM take longer than it expects (64 x 7168 x 2048 bf16: 9 and 7 us expected,
 // 17 and 13 taken).
-// `tiles`: bit mask of the tiles that the product has kernels for.
-inline GemmPlan plan_gemm(bool f32, unsigned tiles, bool dual, int64_t M, int64_t N, int64_t K,
+// `tiles`: bit mask of the tiles that the product has kernels for. `type`: the operands'
+// (false and true: bf16 and fp32).
+enum { kPlanBf16 = 0, kPlanF32 = 1, kPlanI8 = 2 };
+inline GemmPlan plan_gemm(int type, unsigned tiles, bool dual, int64_t M, int64_t N, int64_t K,
                           int pairs) {
   GemmPlan best = {};
   float best_ns = 3.0e38f;
-  const int n = f32 ? 3 : 5;
+  const int n = type == kPlanF32 ? 3 : 5;
   for (int t = 0; t < n; ++t) {
     if (!(tiles >> t & 1)) continue;
-    const TileCost& c = f32 ? kF32Tiles[t] : kBfTiles[t];
+    const TileCost& c = type == kPlanF32  ? kF32Tiles[t]
+                        : type == kPlanI8 ? kI8Tiles[t]
+                                          : kBfTiles[t];
     GemmPlan p = {};
     p.tile = t;
     p.stages = (int)((K + c.bk - 1) / c.bk) * pairs;
@@ -107,7 +118,7 @@ void launch_tile(const GemmArgs& g, const EP& ep, hipStream_t st) {
   if (g.splits > 1) {
     const int64_t n = g.M * ((g.N + 3) / 4);
     const int64_t b = (n + 255) / 256;
-    gemm_join_kernel<Core::DUAL, EP><<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(g, ep);
+    gemm_join_kernel<Core::DUAL, typename Core::Val, EP><<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(g, ep);
   }
 }
 

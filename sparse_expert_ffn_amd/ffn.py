@@ -1,5 +1,5 @@
-"""Binding of include/moe_ffn.h: layer norm, the dense gated feed-forward block
-and products with 4-bit weights, with the names of the C ABI.
+"""Binding of include/moe_ffn.h: layer norm, the dense gated feed-forward block,
+products with 4-bit weights and products in 8-bit integers, with the names of the C ABI.
 
 As the layer's binding it only marshals arguments, but it takes device tensors
 only (sizes come from them) and checks their types, shapes, contiguity and
@@ -20,7 +20,10 @@ __all__ = ["moe_ffn_shape", "make_ffn_shape", "moe_layernorm_forward",
            "moe_ffn_forward_workspace_bytes", "moe_ffn_forward",
            "moe_ffn_backward_workspace_bytes", "moe_ffn_backward", "moe_w4_weight_bytes",
            "moe_quantize_w4", "moe_pack_w4_weights", "moe_w4_matvec",
-           "moe_w4_forward_workspace_bytes", "moe_w4_forward"]
+           "moe_w4_forward_workspace_bytes", "moe_w4_forward", "moe_i8_weight_bytes",
+           "moe_quantize_i8", "moe_pack_i8_weights", "moe_quantize_i8_rows",
+           "moe_i8_matmul_workspace_bytes", "moe_i8_matmul", "moe_i8_ffn_workspace_bytes",
+           "moe_i8_ffn_forward"]
 
 # names of the entry points declared in include/moe_ffn.h
 FFN_EXPORTS = tuple(n for n in __all__ if n not in ("moe_ffn_shape", "make_ffn_shape"))
@@ -58,6 +61,14 @@ def bind(lib) -> None:
         "moe_w4_matvec": [i64, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp],
         "moe_w4_forward_workspace_bytes": [sp],
         "moe_w4_forward": [sp, i32] + [vp] * 11 + [sz, vp],
+        "moe_i8_weight_bytes": [i64, i64, i64],
+        "moe_quantize_i8": [vp, i64, i64, i64, i32, vp, vp, vp],
+        "moe_pack_i8_weights": [vp, vp, i64, i64, i64, vp, vp],
+        "moe_quantize_i8_rows": [vp, i64, i64, i32, vp, vp, vp],
+        "moe_i8_matmul_workspace_bytes": [i64, i64, i64],
+        "moe_i8_matmul": [i64, i64, i64, i32, i32] + [vp] * 5 + [sz, vp],
+        "moe_i8_ffn_workspace_bytes": [fp],
+        "moe_i8_ffn_forward": [fp] + [vp] * 6 + [sz, vp],
     }
     for name, args in sig.items():
         if hasattr(lib, name):
@@ -322,5 +333,97 @@ def moe_w4_forward(shape, A, W_up, W_gate, W_down, Ws_up, Ws_gate, Ws_down, topk
             packed("Ws_gate", Ws_gate, (1, H, Ds)), packed("Ws_down", Ws_down, (1, Ds, H)),
             a("topk_ids", topk_ids, (S, k), torch.int32),
             a("topk_weights", topk_weights, (S, k), torch.float32), a("O", O, (S, H), to)]
+    wa, wn = a.workspace(workspace)
+    return a.run(stream, check, *args, wa, wn)
+
+
+# ---------------------------------------------------------------- 8-bit integers
+
+def moe_i8_weight_bytes(E: int, K: int, N: int) -> int:
+    """Bytes of E matrices [K][N] packed for the 8-bit products (0: unsupported)."""
+    return int(load_library().moe_i8_weight_bytes(E, K, N))
+
+
+def moe_quantize_i8(W, codes, scales, stream=None, check=True) -> int:
+    """Codes (int8, W's shape) and scales (float32, one per column: [..][N]) of a
+    bfloat16 or float32 tensor W [E][K][N] or [K][N]."""
+    a = _Args("moe_quantize_i8")
+    E, K, N = _ekn(a.call, "W", W)
+    dt = _float_dtype(a.call, "W", W)
+    return a.run(stream, check, a("W", W), E, K, N, dt, a("codes", codes, W.shape, torch.int8),
+                 a("scales", scales, (*W.shape[:-2], N), torch.float32))
+
+
+def moe_pack_i8_weights(codes, scales, packed, stream=None, check=True) -> int:
+    """Codes [E][K][N] or [K][N] and scales [..][N] laid out for the products, into
+    ``packed`` (moe_i8_weight_bytes(E, K, N) bytes, uint8)."""
+    a = _Args("moe_pack_i8_weights")
+    E, K, N = _ekn(a.call, "codes", codes)
+    need = moe_i8_weight_bytes(E, K, N)
+    return a.run(stream, check, a("codes", codes, dtype=torch.int8),
+                 a("scales", scales, (*codes.shape[:-2], N), torch.float32), E, K, N,
+                 a("packed", packed, (need,) if need else None, torch.uint8))
+
+
+def moe_quantize_i8_rows(X, codes, scales, stream=None, check=True) -> int:
+    """Codes [S][K] (int8) and scales [S] (float32) of the rows of X [S][K]."""
+    a = _Args("moe_quantize_i8_rows")
+    S, K = _matrix(a.call, "X", X)
+    dt = _float_dtype(a.call, "X", X)
+    return a.run(stream, check, a("X", X), S, K, dt, a("codes", codes, X.shape, torch.int8),
+                 a("scales", scales, (S,), torch.float32))
+
+
+def _i8_weight(a, name, w, want, optional=False):
+    """Address of a layer.I8Weight of E, K, N ``want``."""
+    if w is None and optional:
+        return None
+    if not hasattr(w, "packed") or hasattr(w, "group"):
+        raise TypeError(f"{a.call}: {name} must be an I8Weight, not {type(w).__name__}")
+    if (w.E, w.K, w.N) != want:
+        raise ValueError(f"{a.call}: {name} is {w}, not {want}")
+    return a(name, w.packed, (w.nbytes,), torch.uint8)
+
+
+def moe_i8_matmul_workspace_bytes(S: int, K: int, N: int) -> int:
+    return int(load_library().moe_i8_matmul_workspace_bytes(S, K, N))
+
+
+def moe_i8_matmul(X, W, Y, workspace, row_scales=None, stream=None, check=True) -> int:
+    """Y [S][N] = X W in 8-bit integers, W a layer.I8Weight of one matrix. X [S][K]
+    bfloat16 or float32 (quantised by the call), or int8 codes with ``row_scales`` [S]
+    float32. Y is of X's type or float32 (codes: either)."""
+    a = _Args("moe_i8_matmul")
+    S, K = _matrix(a.call, "X", X)
+    out = _float_dtype(a.call, "Y", Y)
+    if row_scales is None:
+        dt = _float_dtype(a.call, "X", X)
+        if dt == MOE_F32 and out != MOE_F32:
+            raise ValueError("moe_i8_matmul: Y is torch.bfloat16, X torch.float32")
+        flags = MOE_OUTPUT_F32 if out != dt else 0
+    else:
+        dt, flags = out, 0
+    N = getattr(W, "N", 0)
+    args = [S, K, N, dt, flags, a("X", X, None, torch.int8 if row_scales is not None else None),
+            a("row_scales", row_scales, (S,), torch.float32, optional=True),
+            _i8_weight(a, "W", W, (1, K, N)), a("Y", Y, (S, N))]
+    wa, wn = a.workspace(workspace)
+    return a.run(stream, check, *args, wa, wn)
+
+
+def moe_i8_ffn_workspace_bytes(shape) -> int:
+    return int(load_library().moe_i8_ffn_workspace_bytes(ctypes.byref(shape)))
+
+
+def moe_i8_ffn_forward(shape, X, W_up, W_gate, W_down, O, workspace, stream=None,
+                       check=True) -> int:
+    """O = (SiLU(X W_up) * (X W_gate)) W_down, the products in 8-bit integers (weights:
+    layer.I8Weight)."""
+    a = _Args("moe_i8_ffn_forward")
+    S, H, D, t = shape.S, shape.H, shape.D, _types(shape.dtype)
+    to = torch.float32 if shape.flags & MOE_OUTPUT_F32 else t
+    args = [ctypes.byref(shape), a("X", X, (S, H), t), _i8_weight(a, "W_up", W_up, (1, H, D)),
+            _i8_weight(a, "W_gate", W_gate, (1, H, D)),
+            _i8_weight(a, "W_down", W_down, (1, D, H)), a("O", O, (S, H), to)]
     wa, wn = a.workspace(workspace)
     return a.run(stream, check, *args, wa, wn)

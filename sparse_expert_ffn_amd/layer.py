@@ -1,7 +1,8 @@
 """Device buffers for one layer shape, and the C-ABI calls in order: the MoE
 layer (MoEBuffers), its experts with 4-bit weights (W4MoEBuffers), the dense
 gated feed-forward block (FFNBuffers) and layer norm (LayerNormBuffers), the last
-two with their backward passes.
+two with their backward passes, and products and the gated block in 8-bit integers
+(I8LinearBuffers, I8FFNBuffers).
 
 Allocation (torch, device memory) happens once in the constructor; ``run``,
 ``forward`` and ``backward`` only enqueue the library's calls on the stream, so
@@ -16,8 +17,11 @@ from . import (MOE_BF16, MOE_F32, MOE_MXFP8, make_ffn_shape, make_shape, moe_ali
                moe_align_workspace_bytes, moe_ffn_backward, moe_ffn_backward_workspace_bytes,
                moe_ffn_forward, moe_ffn_forward_workspace_bytes, moe_forward,
                moe_forward_workspace_bytes, moe_gate_topk, moe_gate_workspace_bytes,
+               moe_i8_ffn_forward, moe_i8_ffn_workspace_bytes, moe_i8_matmul,
+               moe_i8_matmul_workspace_bytes, moe_i8_weight_bytes,
                moe_layernorm_backward, moe_layernorm_backward_workspace_bytes,
-               moe_layernorm_forward, moe_pack_w4_weights, moe_quantize_w4, moe_w4_forward,
+               moe_layernorm_forward, moe_pack_i8_weights, moe_pack_w4_weights,
+               moe_quantize_i8, moe_quantize_w4, moe_w4_forward,
                moe_w4_forward_workspace_bytes, moe_w4_weight_bytes)
 
 
@@ -252,3 +256,68 @@ class W4MoEBuffers:
         """One pass of the whole layer: gate, top-k, experts, combine."""
         self.route(A, W_router, router_bias, logits_in, stream)
         return self.forward(A, W_up, W_gate, W_down, Ws_up, Ws_gate, Ws_down, stream=stream)
+
+
+class I8Weight:
+    """A weight [E][K][N] or [K][N] as 8-bit codes and a scale per column, packed for the
+    products (codes and scales are not kept). Streams and releases as with W4Weight."""
+
+    def __init__(self, codes, scales, stream=None):
+        self.E, self.K, self.N = (1, *codes.shape) if codes.dim() == 2 else tuple(codes.shape)
+        self.nbytes = moe_i8_weight_bytes(self.E, self.K, self.N)
+        stream = _as_stream(stream, codes.device)
+        with torch.cuda.stream(stream):
+            self.packed = torch.empty(self.nbytes, dtype=torch.uint8, device=codes.device)
+            moe_pack_i8_weights(codes, scales, self.packed, stream)
+        if stream is not None:
+            codes.record_stream(stream)
+            scales.record_stream(stream)
+            self.packed.record_stream(torch.cuda.current_stream(codes.device))
+
+    @classmethod
+    def quantize(cls, W, stream=None):
+        """The library's quantisation of a bf16 or fp32 tensor."""
+        stream = _as_stream(stream, W.device)
+        # the codes and scales are given back when this returns: they belong to the
+        # stream that the two calls run on, so that nothing reuses them before
+        with torch.cuda.stream(stream):
+            codes = torch.empty(W.shape, dtype=torch.int8, device=W.device)
+            scales = torch.empty((*W.shape[:-2], W.shape[-1]), dtype=torch.float32,
+                                 device=W.device)
+            moe_quantize_i8(W, codes, scales, stream)
+        if stream is not None:
+            W.record_stream(stream)
+        return cls(codes, scales, stream)
+
+    def __repr__(self):
+        return f"I8Weight(E={self.E}, K={self.K}, N={self.N})"
+
+
+class I8LinearBuffers:
+    """Y = X W in 8-bit integers, X [S][K] of dtype."""
+
+    def __init__(self, S, K, N, dtype=MOE_BF16, out_f32=False, device="cuda"):
+        t = torch.float32 if out_f32 else _dtype(dtype)
+        self.Y = torch.empty((S, N), dtype=t, device=device)
+        self.ws = torch.empty(moe_i8_matmul_workspace_bytes(S, K, N), dtype=torch.uint8,
+                              device=device)
+
+    def run(self, X, W, row_scales=None, stream=None):
+        """X of dtype, or codes with row_scales (moe_quantize_i8_rows)."""
+        moe_i8_matmul(X, W, self.Y, self.ws, row_scales, stream)
+        return self.Y
+
+
+class I8FFNBuffers:
+    """The dense gated feed-forward block in 8-bit integers."""
+
+    def __init__(self, S, H, D, dtype=MOE_BF16, out_f32=False, device="cuda"):
+        self.shape = make_ffn_shape(S, H, D, dtype, out_f32)
+        self.O = torch.empty((S, H), dtype=torch.float32 if out_f32 else _dtype(dtype),
+                             device=device)
+        self.ws = torch.empty(moe_i8_ffn_workspace_bytes(self.shape), dtype=torch.uint8,
+                              device=device)
+
+    def forward(self, X, W_up, W_gate, W_down, stream=None):
+        moe_i8_ffn_forward(self.shape, X, W_up, W_gate, W_down, self.O, self.ws, stream)
+        return self.O
