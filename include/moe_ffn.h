@@ -1,8 +1,8 @@
 /*
  * sparse_expert_ffn_amd — C ABI of the operators around the MoE layer on one
  * MI355X (gfx950) GPU: layer norm, the dense gated feed-forward block with its
- * backward pass, products with 4-bit weights for decode, and products in 8-bit
- * integers.
+ * backward pass, products with 4-bit weights for decode, products in 8-bit
+ * integers, and the whole MoE layer for a few tokens.
  *
  * The conventions are those of moe.h: device pointers to dense row-major
  * arrays, every call validates on the host, enqueues kernels on `stream` (of
@@ -237,6 +237,50 @@ size_t moe_i8_ffn_workspace_bytes(const moe_ffn_shape* shape); /* 0 if unsupport
 moe_status moe_i8_ffn_forward(const moe_ffn_shape* shape, const void* X, const void* W_up,
                               const void* W_gate, const void* W_down, void* O, void* workspace,
                               size_t workspace_bytes, void* stream);
+
+/*
+ * The whole MoE layer for a few tokens (decode), in two launches: gate scores, softmax
+ * top-k, the experts, the shared expert and the combine.
+ *   G = A W_router (+ router_bias); topk_ids, topk_weights from G as moe_gate_topk's
+ *   O_t = sum_j topk_weights[t][j] FFN_{topk_ids[t][j]}(A_t)  (+ FFN_shared(A_t))
+ * in slot order, then the shared expert. An expert's weights are read once per 16 of
+ * its rows.
+ *   shape        dtype MOE_F32 or MOE_BF16, capacity 0, flags 0 or MOE_OUTPUT_F32, S at
+ *                most 128, E at most 1024, k at most 32; block_size is not looked at
+ *   A            [S][H];  W_router [H][E];  router_bias [E] fp32 or NULL
+ *   W_up, W_gate [E][H][D];  W_down [E][D][H];  Ws_up, Ws_gate [H][D_shared], Ws_down
+ *                [D_shared][H], NULL iff D_shared = 0
+ *   topk_ids     [S][k] int32, topk_weights [S][k] fp32. Outputs; with W_router NULL (and
+ *                then router_bias) inputs: the routing is given, an id outside [0, E) is
+ *                a slot without an expert (it contributes nothing, whatever its weight)
+ *   O            [S][H] dtype, or fp32 with MOE_OUTPUT_F32
+ * Scores are summed in fp32 over up to 256 values of H, these sums in double, and
+ * rounded to fp32; a NaN score ranks as -inf. Sums of the products are fp32, in an order
+ * that depends on the shape and on how many experts the tokens have chosen (so the same
+ * call gives the same bits); in bf16 mode h is rounded once to bf16.
+ * H, D, D_shared multiples of 8 up to 65536, one matrix below 0x7F000000 bytes (with 64
+ * rows and columns more), 16-byte aligned arrays (else MOE_ERR_UNSUPPORTED).
+ *
+ * The second launch's workgroups wait for each other's results. A wait never depends on a
+ * workgroup that has not started; should one last some seconds all the same (a GPU that
+ * is taken away meanwhile), the call gives up and the rows of O that are missing are NaN.
+ *
+ * moe_few_i8_forward takes expert weights packed by moe_pack_i8_weights (E matrices; the
+ * shared expert's with E = 1) and computes each expert as moe_i8_ffn_forward does; dtype
+ * MOE_BF16 (A, W_router), H, D, D_shared multiples of 16.
+ */
+size_t moe_few_workspace_bytes(const moe_shape* shape);    /* 0 if unsupported */
+moe_status moe_few_forward(const moe_shape* shape, const void* A, const void* W_router,
+                           const float* router_bias, const void* W_up, const void* W_gate,
+                           const void* W_down, const void* Ws_up, const void* Ws_gate,
+                           const void* Ws_down, int32_t* topk_ids, float* topk_weights, void* O,
+                           void* workspace, size_t workspace_bytes, void* stream);
+size_t moe_few_i8_workspace_bytes(const moe_shape* shape); /* 0 if unsupported */
+moe_status moe_few_i8_forward(const moe_shape* shape, const void* A, const void* W_router,
+                              const float* router_bias, const void* W_up, const void* W_gate,
+                              const void* W_down, const void* Ws_up, const void* Ws_gate,
+                              const void* Ws_down, int32_t* topk_ids, float* topk_weights,
+                              void* O, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,5 +1,6 @@
 """Binding of include/moe_ffn.h: layer norm, the dense gated feed-forward block,
-products with 4-bit weights and products in 8-bit integers, with the names of the C ABI.
+products with 4-bit weights, products in 8-bit integers and the whole MoE layer for a few
+tokens, with the names of the C ABI.
 
 As the layer's binding it only marshals arguments, but it takes device tensors
 only (sizes come from them) and checks their types, shapes, contiguity and
@@ -23,7 +24,8 @@ __all__ = ["moe_ffn_shape", "make_ffn_shape", "moe_layernorm_forward",
            "moe_w4_forward_workspace_bytes", "moe_w4_forward", "moe_i8_weight_bytes",
            "moe_quantize_i8", "moe_pack_i8_weights", "moe_quantize_i8_rows",
            "moe_i8_matmul_workspace_bytes", "moe_i8_matmul", "moe_i8_ffn_workspace_bytes",
-           "moe_i8_ffn_forward"]
+           "moe_i8_ffn_forward", "moe_few_workspace_bytes", "moe_few_forward",
+           "moe_few_i8_workspace_bytes", "moe_few_i8_forward"]
 
 # names of the entry points declared in include/moe_ffn.h
 FFN_EXPORTS = tuple(n for n in __all__ if n not in ("moe_ffn_shape", "make_ffn_shape"))
@@ -69,6 +71,10 @@ def bind(lib) -> None:
         "moe_i8_matmul": [i64, i64, i64, i32, i32] + [vp] * 5 + [sz, vp],
         "moe_i8_ffn_workspace_bytes": [fp],
         "moe_i8_ffn_forward": [fp] + [vp] * 6 + [sz, vp],
+        "moe_few_workspace_bytes": [sp],
+        "moe_few_forward": [sp] + [vp] * 13 + [sz, vp],
+        "moe_few_i8_workspace_bytes": [sp],
+        "moe_few_i8_forward": [sp] + [vp] * 13 + [sz, vp],
     }
     for name, args in sig.items():
         if hasattr(lib, name):
@@ -427,3 +433,56 @@ def moe_i8_ffn_forward(shape, X, W_up, W_gate, W_down, O, workspace, stream=None
             _i8_weight(a, "W_down", W_down, (1, D, H)), a("O", O, (S, H), to)]
     wa, wn = a.workspace(workspace)
     return a.run(stream, check, *args, wa, wn)
+
+
+# ---------------------------------------------------------------- the layer for a few tokens
+
+def moe_few_workspace_bytes(shape) -> int:
+    return int(load_library().moe_few_workspace_bytes(ctypes.byref(shape)))
+
+
+def moe_few_i8_workspace_bytes(shape) -> int:
+    return int(load_library().moe_few_i8_workspace_bytes(ctypes.byref(shape)))
+
+
+def _few(call, weight, shape, A, W_router, router_bias, W_up, W_gate, W_down, Ws_up, Ws_gate,
+         Ws_down, topk_ids, topk_weights, O, workspace, stream, check):
+    a = _Args(call)
+    S, H, D, Ds, E, k = (shape.S, shape.H, shape.D, shape.D_shared, shape.E, shape.k)
+    t = _types(shape.dtype)
+    to = torch.float32 if shape.flags & MOE_OUTPUT_F32 else t
+    args = [ctypes.byref(shape), a("A", A, (S, H), t),
+            a("W_router", W_router, (H, E), t, optional=True),
+            a("router_bias", router_bias, (E,), torch.float32, optional=True),
+            weight(a, "W_up", W_up, (E, H, D), False), weight(a, "W_gate", W_gate, (E, H, D), False),
+            weight(a, "W_down", W_down, (E, D, H), False), weight(a, "Ws_up", Ws_up, (1, H, Ds), True),
+            weight(a, "Ws_gate", Ws_gate, (1, H, Ds), True),
+            weight(a, "Ws_down", Ws_down, (1, Ds, H), True),
+            a("topk_ids", topk_ids, (S, k), torch.int32),
+            a("topk_weights", topk_weights, (S, k), torch.float32), a("O", O, (S, H), to)]
+    wa, wn = a.workspace(workspace)
+    return a.run(stream, check, *args, wa, wn)
+
+
+def moe_few_forward(shape, A, W_router, router_bias, W_up, W_gate, W_down, Ws_up, Ws_gate,
+                    Ws_down, topk_ids, topk_weights, O, workspace, stream=None,
+                    check=True) -> int:
+    """The whole MoE layer for up to 128 tokens: router, experts, shared expert (its weights
+    [H][D_shared], [D_shared][H]; None without one), combine. topk_ids and topk_weights are
+    written; with W_router None they are the routing."""
+    t = _types(shape.dtype)
+
+    def weight(a, name, w, ekn, optional):
+        return a(name, w, ekn[1:] if optional else ekn, t, optional=optional)
+
+    return _few("moe_few_forward", weight, shape, A, W_router, router_bias, W_up, W_gate, W_down,
+                Ws_up, Ws_gate, Ws_down, topk_ids, topk_weights, O, workspace, stream, check)
+
+
+def moe_few_i8_forward(shape, A, W_router, router_bias, W_up, W_gate, W_down, Ws_up, Ws_gate,
+                       Ws_down, topk_ids, topk_weights, O, workspace, stream=None,
+                       check=True) -> int:
+    """moe_few_forward with the experts' weights in 8 bits (layer.I8Weight each)."""
+    return _few("moe_few_i8_forward", _i8_weight, shape, A, W_router, router_bias, W_up, W_gate,
+                W_down, Ws_up, Ws_gate, Ws_down, topk_ids, topk_weights, O, workspace, stream,
+                check)

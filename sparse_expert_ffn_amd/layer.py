@@ -1,8 +1,9 @@
 """Device buffers for one layer shape, and the C-ABI calls in order: the MoE
 layer (MoEBuffers), its experts with 4-bit weights (W4MoEBuffers), the dense
 gated feed-forward block (FFNBuffers) and layer norm (LayerNormBuffers), the last
-two with their backward passes, and products and the gated block in 8-bit integers
-(I8LinearBuffers, I8FFNBuffers).
+two with their backward passes, products and the gated block in 8-bit integers
+(I8LinearBuffers, I8FFNBuffers), and the whole MoE layer for a few tokens
+(FewMoEBuffers).
 
 Allocation (torch, device memory) happens once in the constructor; ``run``,
 ``forward`` and ``backward`` only enqueue the library's calls on the stream, so
@@ -14,7 +15,9 @@ from __future__ import annotations
 import torch
 
 from . import (MOE_BF16, MOE_F32, MOE_MXFP8, make_ffn_shape, make_shape, moe_align_block_size,
-               moe_align_workspace_bytes, moe_ffn_backward, moe_ffn_backward_workspace_bytes,
+               moe_align_workspace_bytes, moe_few_forward, moe_few_i8_forward,
+               moe_few_i8_workspace_bytes, moe_few_workspace_bytes, moe_ffn_backward,
+               moe_ffn_backward_workspace_bytes,
                moe_ffn_forward, moe_ffn_forward_workspace_bytes, moe_forward,
                moe_forward_workspace_bytes, moe_gate_topk, moe_gate_workspace_bytes,
                moe_i8_ffn_forward, moe_i8_ffn_workspace_bytes, moe_i8_matmul,
@@ -320,4 +323,38 @@ class I8FFNBuffers:
 
     def forward(self, X, W_up, W_gate, W_down, stream=None):
         moe_i8_ffn_forward(self.shape, X, W_up, W_gate, W_down, self.O, self.ws, stream)
+        return self.O
+
+
+class FewMoEBuffers:
+    """The whole MoE layer for up to 128 tokens in two launches. i8: expert weights in 8
+    bits (I8Weight; dtype MOE_BF16)."""
+
+    def __init__(self, S, H, D, E, k, D_shared=0, renormalize=1, dtype=MOE_BF16, i8=False,
+                 out_f32=False, device="cuda"):
+        self.shape = make_shape(S, H, D, E, k, D_shared, renormalize=renormalize, dtype=dtype,
+                                out_f32=out_f32)
+        f32 = torch.float32
+        self.topk_ids = torch.empty((S, k), dtype=torch.int32, device=device)
+        self.topk_weights = torch.empty((S, k), dtype=f32, device=device)
+        self.O = torch.empty((S, H), dtype=f32 if out_f32 else _dtype(dtype), device=device)
+        size, self._call = ((moe_few_i8_workspace_bytes, moe_few_i8_forward) if i8
+                            else (moe_few_workspace_bytes, moe_few_forward))
+        self.ws = torch.empty(size(self.shape), dtype=torch.uint8, device=device)
+
+    def forward(self, A, W_up, W_gate, W_down, Ws_up=None, Ws_gate=None, Ws_down=None,
+                topk_ids=None, topk_weights=None, stream=None):
+        """The experts on a given routing (by default the buffers' own, as run left it); an
+        id outside [0, E) is a slot without an expert."""
+        self._call(self.shape, A, None, None, W_up, W_gate, W_down, Ws_up, Ws_gate, Ws_down,
+                   self.topk_ids if topk_ids is None else topk_ids,
+                   self.topk_weights if topk_weights is None else topk_weights, self.O, self.ws,
+                   stream)
+        return self.O
+
+    def run(self, A, W_router, W_up, W_gate, W_down, Ws_up=None, Ws_gate=None, Ws_down=None,
+            router_bias=None, stream=None):
+        """One pass of the whole layer; topk_ids and topk_weights hold its routing."""
+        self._call(self.shape, A, W_router, router_bias, W_up, W_gate, W_down, Ws_up, Ws_gate,
+                   Ws_down, self.topk_ids, self.topk_weights, self.O, self.ws, stream)
         return self.O
