@@ -239,7 +239,7 @@ moe_status moe_i8_ffn_forward(const moe_ffn_shape* shape, const void* X, const v
                               size_t workspace_bytes, void* stream);
 
 /*
- * The whole MoE layer for a few tokens (decode), in two launches: gate scores, softmax
+ * The whole MoE layer for a few tokens (decode), in three launches: gate scores, softmax
  * top-k, the experts, the shared expert and the combine.
  *   G = A W_router (+ router_bias); topk_ids, topk_weights from G as moe_gate_topk's
  *   O_t = sum_j topk_weights[t][j] FFN_{topk_ids[t][j]}(A_t)  (+ FFN_shared(A_t))

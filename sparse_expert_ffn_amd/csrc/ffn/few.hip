@@ -1,30 +1,36 @@
-// The whole MoE layer for a few tokens in two launches (include/moe_ffn.h).
+// The whole MoE layer for a few tokens in three launches (include/moe_ffn.h).
 //
 // Decode is bound by the chosen experts' bytes, and at one token by how many times the
 // device has to start and finish something.
-//   route    (512 rows of H, 64 experts, 16 tokens)  the router's partial scores; clears
-//            what the next launch counts with
-//   experts  (entry, 64 or 128 columns of D)  h = SiLU(a Wu) * (a Wg) for its columns, then
-//            at once their share of the down product, y = h Wd over all of H
-// An entry is an expert with its rows, or the shared expert with 16 tokens. A workgroup of
-// the second launch needs no other's h: what it would have to wait for is summed instead.
-// The last of an entry's workgroups to arrive adds their shares, the last of a token's
-// entries forms the token's output. Nothing waits: whatever else runs on the device, and in
-// whatever order workgroups start, each runs to its end. (As one grid of tasks that waited
-// for each other's h, with claims from counters, a token took 87 us: a wait, a claim or a
-// count is 1 to 2 us of memory latency, and there were eight in a row.)
+//   route   (512 rows of H, 128 experts, 16 tokens)  the router's partial scores; clears what
+//           the next launches count with
+//   up      (entry, 128 columns of D, part of H)     h = SiLU(a Wu) * (a Wg)
+//   down    (entry, 128 or 256 columns of H)         y = h Wd, and O for the tokens that it
+//           completes
+// An entry is an expert with its rows, or the shared expert with 16 tokens. Up to 8 tokens
+// every workgroup of `up` sums the scores and selects the top-k for itself; beyond, a launch
+// of its own does it (one workgroup per token).
 //
-// Up to 8 tokens every workgroup sums the scores and selects the top-k for itself; beyond,
-// a launch of its own does it (one wave per token). With 8-bit weights h's row scale needs
-// the whole row: the experts' launch becomes two, up/gate and down.
+// Within a launch nothing waits: where there are few columns, H is cut in parts, and the last
+// of them to arrive adds the sums; the last of a token's entries to arrive at a column
+// group of H forms the token's output there.
 //
-// Weights go from memory into registers, rows of 128 bytes to 16 lanes, and become MFMA
-// operands there: no LDS on their way. 8 waves: up or gate, 64 columns each, shares of K
-// added through LDS; then 64 columns of H each.
-//   bf16: a lane holds 2 x 8 rows of 4 columns; byte permutes give the operands (8 rows of a
+// Fewer launches were slower (one token, 256 experts of 2048 x 768 top-8; 64 tokens): one grid
+// of tasks that wait for each other's h, claimed from counters: 87 and 507 us, since a claim,
+// a wait or a count is 1 to 2 us of memory latency and there were eight in a row; up and
+// down in one workgroup, each adding its columns' share of y: 47 and 440 us, since at one
+// token 48 workgroups held all of the down product, and with many the last round of long
+// workgroups left the chip half empty.
+//
+// Weights go from memory into registers, rows of 256 bytes to 16 lanes (with 128 the widest
+// layer's weights came at 3.0 TB/s, with two waves side by side at 3.6), and become MFMA
+// operands there: no LDS on their way. 4 waves: up or gate, half of K each; or 1 or 2 column
+// tiles of H, a quarter or half of D each; added through LDS.
+//   bf16: a lane holds 8 rows of 8 columns; byte permutes give the operands (8 rows of a
 //         column) of v_mfma_f32_16x16x32_bf16
-//   fp32: 2 x 4 rows of 4 columns, v_mfma_f32_16x16x4_f32 (K in an order that suits)
-//   int8: packed in operand order, v_mfma_i32_16x16x64_i8
+//   fp32: 4 rows of 2 x 4 columns, v_mfma_f32_16x16x4_f32 (K in an order that suits)
+//   int8: packed in operand order, 64 columns, v_mfma_i32_16x16x64_i8; h's row scale needs the
+//         whole row: the last of an entry's workgroups quantises its rows
 #include "gemm_direct.h"
 #include "i8.h"
 #include "topk.h"
@@ -39,8 +45,13 @@ constexpr int kNonTemporal = 2;      // load hint: weights are read once
 constexpr int64_t kMaxTokens = 128;
 constexpr int64_t kMaxSize = 65536;  // H, D, D_shared
 constexpr int kMaxRows = (int)kMaxTokens * 32;  // assignments
-constexpr int kThreads = 512, kWaves = 8;
-constexpr int kCols = 64;            // columns of a wave
+constexpr int kThreads = 512, kWaves = 8;  // router
+constexpr int kExpertThreads = 256;
+constexpr int kCols = 128;           // columns of a wave
+constexpr int kCols8 = 64;           // with 8-bit weights
+constexpr int kMaxSplits = 8;        // parts of H
+constexpr int kWanted = 512;         // workgroups: as many as the chip holds
+constexpr int kSplitRows = 64;       // assignments up to which it is cut
 constexpr int kRouteRows = 512;      // K rows of a router workgroup, 64 to a wave
 constexpr int kOwnRoute = 8;         // tokens that each workgroup routes for itself
 
@@ -54,18 +65,23 @@ struct FewArgs {
   float* tw;
   void* O;
   float* score;        // [route splits][S][E]
-  int* entry_done;     // [entries + shared] arrived column groups
-  int* token_done;     // [S] arrived entries
-  uint32_t* top;       // int8: [F + S] abs_bits of the largest h
-  int n_words;         // of these three
+  int* entry_done;     // [entries + shared] int8: arrived column groups of each 16 rows
+  int* split_done;     // [column groups][rounds of 16 rows] arrived parts of H
+  int* token_done;     // [S][column groups of H] arrived entries
+  int n_words;         // of these
   int8_t* xc;          // int8: codes and scales of the tokens
   float* xs;
-  float* h;            // int8: [F][D], then [S][Ds]
-  float* y;            // [slices][F + S][H]
+  char* h;             // [F][D], then [S][Ds] (fp32 with 8-bit weights)
+  int8_t* hc;          // int8: its codes and scales
+  float* hs;
+  char* part;          // [column groups][splits][F + S][2][columns]
+  float* y;            // [F + S][H]
   int S, H, D, Ds, E, k, F;
   int by_row, entries; // an entry per assignment (the first of its expert), or per expert
   int shared;          // shared entries
   int slices, slices_s;  // column groups of D
+  int splits, rounds;  // parts of H; rounds of 16 rows at most
+  int cols;            // column groups of H
   int route_splits, renormalize, out_f32;
   int routed;          // ids and tw are there (given, or by a launch before)
 };
@@ -117,28 +133,29 @@ struct Kind<kBf16> {
   using T = bf16_t;     // activations
   using Val = float;
   using Acc = f32x4_t;
-  static constexpr int ES = 2, STEP = 64, NX = 2;  // bytes of a weight, K rows per step
+  static constexpr int ES = 2, STEP = 32, COLS = kCols;  // bytes of a weight, K per step
 };
 template <>
 struct Kind<kF32> {
   using T = float;
   using Val = float;
   using Acc = f32x4_t;
-  static constexpr int ES = 4, STEP = 32, NX = 2;
+  static constexpr int ES = 4, STEP = 16, COLS = kCols;
 };
 template <>
 struct Kind<kI8> {
   using T = bf16_t;
   using Val = int;
   using Acc = i32x4_t;
-  static constexpr int NX = 1;
+  static constexpr int ES = 1, STEP = 64, COLS = kCols8;
 };
 
-// 64 columns of a matrix [K][N] from n0 on; K values from k0 on.
+// A wave's columns of a matrix [K][N] from n0 on, K values from k0 on.
 template <int P>
 struct Columns {
   rsrc_t r;
   uint32_t off, row, step;
+  uint32_t past[P == kF32 ? 2 : 1];  // fp32: two halves of 64 columns, which end at N each
 
   __device__ __forceinline__ Columns() {}
   __device__ __forceinline__ Columns(const char* matrix, int K, int N, int n0, int k0 = 0) {
@@ -152,9 +169,13 @@ struct Columns {
     } else {
       constexpr int ES = Kind<P>::ES;
       r = make_rsrc(matrix, (int64_t)K * N * ES);
-      off = n0 + 4 * c < N
-                ? (uint32_t)((k0 + (P == kBf16 ? 8 : 4) * g) * N + n0 + 4 * c) * ES
-                : kPastEnd;
+      off = (uint32_t)((k0 + (P == kBf16 ? 8 : 4) * g) * N + n0 + (P == kBf16 ? 8 : 4) * c) * ES;
+      if constexpr (P == kBf16) {
+        if (n0 + 8 * c >= N) off = kPastEnd;
+      } else {
+        past[0] = n0 + 4 * c < N ? 0 : kPastEnd;
+        past[1] = n0 + 64 + 4 * c < N ? 0 : kPastEnd;
+      }
       row = (uint32_t)N * ES;
       step = row * Kind<P>::STEP;
     }
@@ -164,128 +185,84 @@ struct Columns {
 template <int P>
 struct Step {
   using Acc = typename Kind<P>::Acc;
-  static constexpr int NX = Kind<P>::NX;
-  uint4 w[P == kI8 ? 4 : 8];  // bf16: two rows of 8 bytes each
+  static constexpr int NJ = P == kI8 ? 4 : 8;  // loads, and accumulators
+  uint4 w[NJ];
 
   __device__ __forceinline__ void load(const Columns<P>& m, uint32_t o) {
-    if constexpr (P == kI8) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             m.r, o + j * m.row, 0, kNonTemporal));
-    } else if constexpr (P == kBf16) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t at = o + (uint32_t)(i / 4 * 32 + i % 4 * 2) * m.row;
-        const auto a = __builtin_amdgcn_raw_buffer_load_b64(m.r, at, 0, kNonTemporal);
-        const auto b = __builtin_amdgcn_raw_buffer_load_b64(m.r, at + m.row, 0, kNonTemporal);
-        w[i] = make_uint4(a[0], a[1], b[0], b[1]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i] = __builtin_bit_cast(
-            uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                       m.r, o + (uint32_t)(i / 4 * 16 + i % 4) * m.row, 0, kNonTemporal));
+    for (int i = 0; i < NJ; ++i) {
+      uint32_t at = o + i * m.row;
+      if constexpr (P == kF32) at = (o + (i >> 1) * m.row + (i & 1) * 256) | m.past[i & 1];
+      w[i] = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(m.r, at, 0, kNonTemporal));
     }
   }
-  // Step s of the columns; behind the last one (steps): zeros.
-  __device__ __forceinline__ void load(const Columns<P>& m, int s, int steps) {
-    load(m, s < steps ? m.off + (uint32_t)s * m.step : kPastEnd);
+  // Step s of the columns; from `end` on: zeros.
+  __device__ __forceinline__ void load(const Columns<P>& m, int s, int end) {
+    load(m, s < end ? m.off + (uint32_t)s * m.step : kPastEnd);
   }
-  __device__ __forceinline__ void compute(const uint4 (&x)[NX], Acc (&acc)[4]) const {
+  __device__ __forceinline__ void compute(const uint4& x, Acc (&acc)[NJ]) const {
     if constexpr (P == kBf16) {
+      const bf16x8_t a = __builtin_bit_cast(bf16x8_t, x);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, x[h]);
+      for (int j = 0; j < 8; ++j) {
+        // column j of the lane's 8: rows 2 i and 2 i + 1 in dword i
+        const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
+        uint32_t d[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // column j of the lane's 4: rows 2 i and 2 i + 1 in dword i
-          const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
-          uint32_t d[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            d[i] = __builtin_amdgcn_perm(word(w[4 * h + i], 2 + j / 2), word(w[4 * h + i], j / 2),
-                                         sel);
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              a, __builtin_bit_cast(bf16x8_t, make_uint4(d[0], d[1], d[2], d[3])), acc[j], 0, 0,
-              0);
-        }
+        for (int i = 0; i < 4; ++i)
+          d[i] = __builtin_amdgcn_perm(word(w[2 * i + 1], j / 2), word(w[2 * i], j / 2), sel);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            a, __builtin_bit_cast(bf16x8_t, make_uint4(d[0], d[1], d[2], d[3])), acc[j], 0, 0, 0);
       }
     } else if constexpr (P == kF32) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = __uint_as_float(word(x[i / 4], i % 4));
+      for (int i = 0; i < 4; ++i) {
+        const float a = __uint_as_float(word(x, i));
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, __uint_as_float(word(w[i], j)), acc[j],
-                                                        0, 0, 0);
+        for (int j = 0; j < 8; ++j)
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+              a, __uint_as_float(word(w[2 * i + j / 4], j % 4)), acc[j], 0, 0, 0);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, x[0]),
+        acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, x),
                                                        __builtin_bit_cast(i32x4_t, w[j]), acc[j],
                                                        0, 0, 0);
     }
   }
 };
 
-// 16 rows of the other operand, 64 NX bytes of each per step (lane l: row l % 16, 16 bytes at
-// 16 (l / 16) of every 64); rows that are not there and what lies behind a row's end read
-// as zeros.
+// 16 rows of the other operand, 64 bytes of each per step (lane l: row l % 16, bytes 16 (l
+// / 16) .. + 15); rows that are not there and what lies behind a row's end read as zeros.
 struct Rows {
   rsrc_t r;
   uint32_t off;    // of this lane's row
   uint32_t bytes;  // of a row
-  template <int NX>
-  __device__ __forceinline__ void load(int s, uint4 (&x)[NX]) const {
-#pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      const uint32_t at = (uint32_t)(s * NX + i) * 64 + ((threadIdx.x & 63) >> 4) * 16;
-      x[i] = load16(r, at < bytes ? off + at : kPastEnd);
-    }
+  // step s; from `end` on: zeros
+  __device__ __forceinline__ uint4 load(int s, int end) const {
+    const uint32_t at = (uint32_t)s * 64 + ((threadIdx.x & 63) >> 4) * 16;
+    return load16(r, s < end && at < bytes ? off + at : kPastEnd);
   }
 };
-// int8's h: fp32 rows, quantised as they are read.
-struct QuantRows {
-  rsrc_t r;
-  uint32_t off, bytes;
-  Quant q;
-  struct Raw {
-    uint4 v[4];
-  };
-  __device__ __forceinline__ void load(int s, Raw& x) const {
-    const uint32_t at = ((uint32_t)s * 64 + ((threadIdx.x & 63) >> 4) * 16) * 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x.v[i] = load16(r, at < bytes ? off + at + 16 * i : kPastEnd);
-  }
-  __device__ __forceinline__ void codes(const Raw& x, uint4 (&c)[1]) const {
-    uint32_t d[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      d[i] = q.pack4(__uint_as_float(x.v[i].x), __uint_as_float(x.v[i].y),
-                     __uint_as_float(x.v[i].z), __uint_as_float(x.v[i].w));
-    c[0] = make_uint4(d[0], d[1], d[2], d[3]);
-  }
-};
-
-// Rows 4 (l / 16) + r and columns of the accumulators that a lane holds: 4 c .. + 3 (int8: c,
-// 16 + c, ..) of the wave's 64.
+// This lane's sums into LDS as rows of the wave's columns: rows 4 (l / 16) .. + 3 below n.
 template <int P>
-__device__ __forceinline__ void put_sums(const typename Kind<P>::Acc (&acc)[4],
+__device__ __forceinline__ void put_sums(const typename Kind<P>::Acc (&acc)[Step<P>::NJ],
                                          typename Kind<P>::Val* to, int n) {
+  using Acc = typename Kind<P>::Acc;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (4 * g + r >= n) continue;
-    typename Kind<P>::Val* row = to + (4 * g + r) * kCols;
+    typename Kind<P>::Val* row = to + (4 * g + r) * Kind<P>::COLS;
     if constexpr (P == kI8) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) row[16 * j + c] = acc[j][r];
     } else {
-      *reinterpret_cast<typename Kind<P>::Acc*>(row + 4 * c) =
-          typename Kind<P>::Acc{acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
+      const int at0 = P == kBf16 ? 8 * c : 4 * c, at1 = P == kBf16 ? 8 * c + 4 : 64 + 4 * c;
+      *reinterpret_cast<Acc*>(row + at0) = Acc{acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
+      *reinterpret_cast<Acc*>(row + at1) = Acc{acc[4][r], acc[5][r], acc[6][r], acc[7][r]};
     }
   }
 }
@@ -304,18 +281,18 @@ __device__ __forceinline__ void load_router(Step<P>& st, const Columns<P>& m, in
   for (int i = 0; i < 8; ++i) {
     uint32_t d[4];
     if constexpr (P == kBf16) {
+      const int k = s * 32 + 8 * g + i;
 #pragma unroll
-      for (int v = 0; v < 8; ++v) {  // two rows of 4
-        const int k = s * 64 + i / 4 * 32 + 8 * g + i % 4 * 2 + v / 4;
-        const uint32_t b =
-            __builtin_amdgcn_raw_buffer_load_b16(m.r, at(k, n0 + 4 * c + v % 4), 0, 0);
+      for (int v = 0; v < 8; ++v) {
+        const uint32_t b = __builtin_amdgcn_raw_buffer_load_b16(m.r, at(k, n0 + 8 * c + v), 0, 0);
         d[v / 2] = v & 1 ? d[v / 2] | b << 16 : b;
       }
     } else {
-      const int k = s * 32 + i / 4 * 16 + 4 * g + i % 4;
+      const int k = s * 16 + 4 * g + i / 2;
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        d[v] = __builtin_amdgcn_raw_buffer_load_b32(m.r, at(k, n0 + 4 * c + v), 0, 0);
+        d[v] = __builtin_amdgcn_raw_buffer_load_b32(m.r, at(k, n0 + 64 * (i & 1) + 4 * c + v), 0,
+                                                    0);
     }
     st.w[i] = make_uint4(d[0], d[1], d[2], d[3]);
   }
@@ -348,16 +325,16 @@ __global__ __launch_bounds__(kThreads) void few_route_kernel(FewArgs p, int bloc
     const Rows a = {make_rsrc(p.A, (int64_t)p.S * bytes), row < p.S ? row * bytes : kPastEnd,
                     bytes};
     Step<P> st[STEPS];
-    uint4 x[STEPS][Kind<P>::NX];
+    uint4 x[STEPS];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       if constexpr (VEC)
         st[s].load(m, s0 + s, steps);
       else
         load_router<P>(st[s], m, s0 + s, p.H, p.E, n0);
-      a.load(s0 + s, x[s]);
+      x[s] = a.load(s0 + s, steps);
     }
-    f32x4_t acc[4] = {};
+    f32x4_t acc[8] = {};
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) st[s].compute(x[s], acc);
     const int n = p.S - 16 * tb < 16 ? p.S - 16 * tb : 16;
@@ -450,7 +427,7 @@ struct Work {
   int n;           // rows
   int expert;      // -1: shared
   int count[2];
-  int done[16];    // tokens complete
+  int done[64];    // tokens complete
   uint16_t rows[kMaxRows];       // assignments (shared: tokens)
   int ids[kOwnRoute * 32];       // of the tokens that this workgroup has routed for itself
   float tw[kOwnRoute * 32];
@@ -458,14 +435,14 @@ struct Work {
 
 // Routes where that is this workgroup's to do, and finds entry y's expert and rows; false:
 // nothing to do. lds: kOwnRoute x 1024 floats.
+template <int THREADS>
 __device__ __forceinline__ bool find_work(const FewArgs& p, int y, bool shared, float* lds,
                                           Work& w) {
   const int tid = threadIdx.x;
   if (!p.routed) {
-    sum_scores(p, 0, p.S, tid, kThreads, lds);
+    sum_scores(p, 0, p.S, tid, THREADS, lds);
     __syncthreads();
-    const int t = uniform(tid >> 6);
-    if (t < p.S)
+    for (int t = uniform(tid >> 6); t < p.S; t += THREADS / 64)
       topk_one(lds + t * p.E, p.E, p.k, p.renormalize, w.ids + t * p.k, w.tw + t * p.k, tid & 63);
     __syncthreads();
     if (blockIdx.x == 0 && tid < p.F) {
@@ -494,12 +471,23 @@ __device__ __forceinline__ bool find_work(const FewArgs& p, int y, bool shared, 
   if (e < 0 || e >= p.E) return false;
   if (tid == 0) w.count[0] = w.count[1] = 0;
   __syncthreads();
-  // in no particular order: rows do not meet in the products
-  for (int f = tid; f < p.F; f += kThreads)
-    if ((here ? w.ids[f] : p.ids[f]) == e) {
-      if (p.by_row && f < y) w.count[1] = 1;  // an earlier entry's
-      w.rows[atomicAdd(&w.count[0], 1)] = (uint16_t)f;
+  if (here) {
+    // in their order: workgroups that share the rows' sums list them alike
+    if (tid < p.F && w.ids[tid] == e) {
+      int at = 0;
+      for (int f = 0; f < tid; ++f) at += w.ids[f] == e;
+      w.rows[at] = (uint16_t)tid;
+      if (p.by_row && tid < y) w.count[1] = 1;  // an earlier entry's
+      atomicAdd(&w.count[0], 1);
     }
+  } else {
+    // in no particular order: rows do not meet in the products
+    for (int f = tid; f < p.F; f += THREADS)
+      if (p.ids[f] == e) {
+        if (p.by_row && f < y) w.count[1] = 1;
+        w.rows[atomicAdd(&w.count[0], 1)] = (uint16_t)f;
+      }
+  }
   if (tid == 0) w.expert = e;
   __syncthreads();
   if (tid == 0) w.n = w.count[0];
@@ -513,362 +501,315 @@ __device__ __forceinline__ bool valid_slot(const FewArgs& p, const Work& w, int 
   return id >= 0 && id < p.E;
 }
 
-// The tokens that this workgroup's entry completes: O_t = sum_j w_tj y_tj (+ the shared row),
-// slots without an expert left out. The entry's rows of y are in memory.
-__device__ __forceinline__ void combine(const FewArgs& p, Work& w) {
+// The tokens whose columns n0 .. + width - 1 this workgroup completes: O_t = sum_j w_tj y_tj (+
+// the shared row), slots without an expert left out. Its own rows of y are in memory.
+template <int THREADS>
+__device__ __forceinline__ void combine(const FewArgs& p, Work& w, int group, int n0, int width) {
   const int tid = threadIdx.x;
   const int n = uniform(w.n);
   const bool shared = uniform(w.expert) < 0;
   const rsrc_t y = make_rsrc(p.y, (int64_t)(p.F + p.S) * p.H * 4);
-  for (int r0 = 0; r0 < n; r0 += 16) {
-    if (tid < 16) {
-      int t = -1;
+  const int quads = (p.H - n0 < width ? p.H - n0 : width) / 4;
+  for (int r0 = 0; r0 < n; r0 += 64) {
+    if (tid < 64) {
+      bool last = false;
+      int tok = 0;
       if (r0 + tid < n) {
-        const int f = w.rows[r0 + tid], tok = shared ? f : f / p.k;
+        const int f = w.rows[r0 + tid];
+        tok = shared ? f : f / p.k;
         int need = p.shared ? 1 : 0;
         for (int j = 0; j < p.k; ++j) need += valid_slot(p, w, tok * p.k + j);
-        if (count_up(p.token_done + tok) == need - 1) t = tok;
+        last = count_up(p.token_done + tok * p.cols + group) == need - 1;
       }
-      w.done[tid] = t;
+      const uint64_t b = __ballot(last);
+      if (last) w.done[__popcll(b & ((1ull << tid) - 1))] = tok;
+      if (tid == 0) w.count[0] = __popcll(b);
     }
     __syncthreads();
-    for (int i = 0; i < 16; ++i) {
-      const int t = uniform(w.done[i]);
-      if (t < 0) continue;
-      for (int c = tid * 4; c < p.H; c += kThreads * 4) {
-        f32x4_t a = {0.f, 0.f, 0.f, 0.f};
-        // 8 slots' loads at a time
-        for (int j0 = 0; j0 < p.k; j0 += 8) {
-          f32x4_t v[8];
+    const int all = uniform(w.count[0]) * quads;
+    for (int i = tid; i < all; i += THREADS) {
+      const int d = i / quads, c = n0 + (i - d * quads) * 4, t = w.done[d];
+      f32x4_t a = {0.f, 0.f, 0.f, 0.f};
+      // 8 slots' loads at a time
+      for (int j0 = 0; j0 < p.k; j0 += 8) {
+        f32x4_t v[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[j] = load_shared(
-                y, j0 + j < p.k ? (uint32_t)((t * p.k + j0 + j) * p.H + c) * 4 : kPastEnd);
+        for (int j = 0; j < 8; ++j)
+          v[j] = load_shared(
+              y, j0 + j < p.k ? (uint32_t)((t * p.k + j0 + j) * p.H + c) * 4 : kPastEnd);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int f = t * p.k + (j0 + j < p.k ? j0 + j : 0);
-            const float wt = p.F <= kOwnRoute * 32 ? w.tw[f] : p.tw[f];
-            const bool in = j0 + j < p.k && valid_slot(p, w, f);
+        for (int j = 0; j < 8; ++j) {
+          const int f = t * p.k + (j0 + j < p.k ? j0 + j : 0);
+          const float wt = p.F <= kOwnRoute * 32 ? w.tw[f] : p.tw[f];
+          const bool in = j0 + j < p.k && valid_slot(p, w, f);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) a[q] = in ? a[q] + wt * v[j][q] : a[q];
-          }
+          for (int q = 0; q < 4; ++q) a[q] = in ? a[q] + wt * v[j][q] : a[q];
         }
-        if (p.shared) {
-          const f32x4_t v = load_shared(y, (uint32_t)((p.F + t) * p.H + c) * 4);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) a[q] += v[q];
-        }
-        const float o[4] = {a[0], a[1], a[2], a[3]};
-        if (p.out_f32)
-          store_n(reinterpret_cast<float*>(p.O) + (int64_t)t * p.H + c, o);
-        else
-          store_n(reinterpret_cast<bf16_t*>(p.O) + (int64_t)t * p.H + c, o);
       }
+      if (p.shared) {
+        const f32x4_t v = load_shared(y, (uint32_t)((p.F + t) * p.H + c) * 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) a[q] += v[q];
+      }
+      const float o[4] = {a[0], a[1], a[2], a[3]};
+      if (p.out_f32)
+        store_n(reinterpret_cast<float*>(p.O) + (int64_t)t * p.H + c, o);
+      else
+        store_n(reinterpret_cast<bf16_t*>(p.O) + (int64_t)t * p.H + c, o);
     }
     __syncthreads();
   }
 }
 
-// This wave's share of K: every shares-th of `steps` steps from `first` on.
-template <int P>
-__device__ __forceinline__ void stream(const Columns<P>& m, const Rows& a, int first, int shares,
-                                       int steps, typename Kind<P>::Acc (&acc)[4]) {
-  constexpr int DEPTH = P == kI8 ? 3 : 2;
-  constexpr int NX = Kind<P>::NX;
+// This wave's share of K's steps below `end`: every SHARES-th from `first` on.
+template <int P, int SHARES, int DEPTH>
+__device__ __forceinline__ void stream(const Columns<P>& m, const Rows& a, int first, int end,
+                                       typename Kind<P>::Acc (&acc)[Step<P>::NJ]) {
   Step<P> st[DEPTH];
-  uint4 x[DEPTH][NX];
+  uint4 x[DEPTH];
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) {
-    st[d].load(m, first + d * shares, steps);
-    a.load(first + d * shares, x[d]);
+    st[d].load(m, first + d * SHARES, end);
+    x[d] = a.load(first + d * SHARES, end);
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) acc[j] = typename Kind<P>::Acc{};
-  for (int s = first; s < steps;) {
+  for (int j = 0; j < Step<P>::NJ; ++j) acc[j] = typename Kind<P>::Acc{};
+  for (int s = first; s < end;) {
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d, s += shares) {
+    for (int d = 0; d < DEPTH; ++d, s += SHARES) {
       st[d].compute(x[d], acc);
-      st[d].load(m, s + DEPTH * shares, steps);
-      a.load(s + DEPTH * shares, x[d]);
+      st[d].load(m, s + DEPTH * SHARES, end);
+      x[d] = a.load(s + DEPTH * SHARES, end);
       __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not behind the next step
     }
   }
 }
 
-// Workgroup (entry, column group of CG x 64): up and gate of its columns (waves: 2 matrices x CG
-// x 4 / CG shares of K), h, and their share of the down product (waves: 64 columns of H).
-// Which entry comes first does not matter; a group's neighbours run at about the same time.
-template <int P, int CG>
-__global__ __launch_bounds__(kThreads, 4) void few_expert_kernel(FewArgs p) {
+// A thread's 4 columns of one or two rows of a round, and their places: rows r1 + i STRIDE.
+template <int P>
+struct Quads {
+  static constexpr int PER_ROW = Kind<P>::COLS / 4;
+  static constexpr int N = 16 * PER_ROW / kExpertThreads, STRIDE = 16 / N;
+};
+
+// Row f's codes and scale from its fp32 values, by one wave (twice read).
+__device__ __forceinline__ void quantize_row(rsrc_t h, uint32_t row, int D, int8_t* codes,
+                                             float* scale) {
+  const int lane = threadIdx.x & 63;
+  uint32_t top = 0;
+  for (int c = lane * 4; c < D; c += 256) {
+    const f32x4_t v = load_shared(h, row + c * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = abs_bits(v[i]);
+      top = top > b ? top : b;
+    }
+  }
+  const Quant q(wave_max_u32(top));
+  if (lane == 0) *scale = q.scale;
+  for (int c = lane * 4; c < D; c += 256) {
+    const f32x4_t v = load_shared(h, row + c * 4);
+    *reinterpret_cast<uint32_t*>(codes + c) = q.pack4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// Workgroup (entry, columns of D, part of H): waves 2 matrices x 2 shares of K.
+template <int P>
+__global__ __launch_bounds__(kExpertThreads, 2) void few_up_kernel(FewArgs p) {
+  using Val = typename Kind<P>::Val;
   using Acc = typename Kind<P>::Acc;
-  constexpr int NX = Kind<P>::NX, STEP = Kind<P>::STEP, ES = Kind<P>::ES;
-  constexpr int SHARES = 4 / CG, W = CG * kCols;
-  constexpr int PITCH = W * ES + 16;  // bytes of a row of h: 16 rows' 16 bytes in all banks
-  __shared__ __align__(16) float red[kWaves * 16 * kCols];
-  __shared__ __align__(16) char hbuf[16 * PITCH];
+  using Q = Quads<P>;
+  constexpr bool I8 = P == kI8;
+  constexpr int COLS = Kind<P>::COLS, STEP = Kind<P>::STEP;
+  constexpr int SHARES = 2, HS = P == kBf16 ? 2 : 4;
+  __shared__ __align__(16) Val red[4 * 16 * kCols];
   __shared__ Work w;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
-  const int64_t routed = (int64_t)p.entries * p.slices;
+  const int64_t routed = (int64_t)p.entries * p.slices * p.splits;
   const bool shared = blockIdx.x >= routed;
   const int slices = shared ? p.slices_s : p.slices;
   const int b = shared ? (int)(blockIdx.x - routed) : (int)blockIdx.x;
-  const int entry = uniform(b / slices), slice = b - entry * slices;
-  if (!find_work(p, entry, shared, red, w)) return;
+  const int group = uniform(b / p.splits), split = b - group * p.splits;
+  const int entry = uniform(group / slices), d0 = (group - entry * slices) * COLS;
+  if (!find_work<kExpertThreads>(p, entry, shared, reinterpret_cast<float*>(red), w)) return;
   const int n = uniform(w.n), e = shared ? 0 : uniform(w.expert);
   const int D = shared ? p.Ds : p.D;
-  const int64_t size = (int64_t)p.H * D * ES;
+  const int64_t size = I8 ? i8_matrix_bytes(p.H, D) : (int64_t)p.H * D * Kind<P>::ES;
   const char* const* mats = shared ? p.ws : p.w;
-  const int mat = wave / 4, part = wave % 4;
-  const int d0 = slice * W;
-  const int steps = (p.H + STEP - 1) / STEP;
-  Columns<P> m(mats[mat] + e * size, p.H, D, d0 + part / SHARES * kCols);
-  const rsrc_t y = make_rsrc(p.y + (int64_t)slice * (p.F + p.S) * p.H,
-                             (int64_t)(p.F + p.S) * p.H * 4);
+  const int steps = (p.H + STEP - 1) / STEP, per = uniform((steps + p.splits - 1) / p.splits);
+  const int end = (split + 1) * per < steps ? (split + 1) * per : steps;
+  Columns<P> m(mats[wave / SHARES] + e * size, p.H, D, d0);
+  const int base = shared ? p.F : 0, at = shared ? p.entries * p.slices + group : group;
+  const rsrc_t h = make_rsrc(p.h + (shared ? (int64_t)p.F * p.D * HS : 0),
+                             (int64_t)(shared ? p.S : p.F) * D * HS);
+  const uint32_t one = (uint32_t)(p.F + p.S) * 2 * COLS * 4;
+  const rsrc_t part = make_rsrc(p.part + (int64_t)at * p.splits * one, (int64_t)p.splits * one);
+  const int r1 = tid / Q::PER_ROW, c = tid % Q::PER_ROW * 4;
   for (int r0 = 0; r0 < n; r0 += 16) {
     const int rows = n - r0 < 16 ? n - r0 : 16;
     const int lr = lane & 15, f = lr < rows ? w.rows[r0 + lr] : 0;
-    const uint32_t bytes = (uint32_t)p.H * ES;
-    const Rows a = {make_rsrc(p.A, (int64_t)p.S * bytes),
+    const uint32_t bytes = (uint32_t)p.H * Kind<P>::ES;
+    const Rows a = {make_rsrc(I8 ? (const void*)p.xc : p.A, (int64_t)p.S * bytes),
                     lr < rows ? (shared ? f : f / p.k) * bytes : kPastEnd, bytes};
-    // (the loads' addresses are formed in each round of 16 rows: kept, they spill)
-    int zero = 0;
-    asm volatile("" : "+v"(m.off));
-    asm volatile("" : "+s"(zero));
-    Acc acc[4];
-    stream<P>(m, a, part % SHARES, SHARES, steps, acc);
-    // the down product's steps: 64 columns of H, the group's rows of D in turn
-    constexpr int KS = W / STEP;
-    const int tiles = (p.H + kCols - 1) / kCols;
-    Step<P> st[2];
-    auto columns = [&](int tile) {
-      return Columns<P>(mats[2] + e * size, D, p.H, tile * kCols, d0 + zero);
-    };
-    Columns<P> next = columns(wave);
-    int nt = wave, nk = 0;
-    auto load = [&](Step<P>& to) {
-      to.load(next, nt < tiles ? next.off + nk * next.step : kPastEnd);
-      if (++nk == KS) {
-        nk = 0;
-        nt += kWaves;
-        if (nt < tiles) next = columns(nt);
-      }
-    };
-    load(st[0]);
-    load(st[1]);
-    put_sums<P>(acc, red + wave * 16 * kCols, rows);
+    asm volatile("" : "+v"(m.off));  // (addresses kept over the rounds spill)
+    Acc acc[Step<P>::NJ];
+    stream<P, SHARES, 3>(m, a, split * per + wave % SHARES, end, acc);
+    put_sums<P>(acc, red + wave * 16 * COLS, rows);
     __syncthreads();
-    // thread: 4 columns of a row; the shares of K in their order
-    for (int i = tid; i < rows * (W / 4); i += kThreads) {
-      const int r = i / (W / 4), c = i % (W / 4) * 4;
-      f32x4_t v[2];
+    // the shares of K in their order, then the parts
+    Acc v[Q::N][2];
+    uint32_t o[Q::N];
+#pragma unroll
+    for (int i = 0; i < Q::N; ++i) {
+      const int r = r1 + i * Q::STRIDE;
+      o[i] = kPastEnd;
+      v[i][0] = v[i][1] = Acc{};
+      if (r >= rows) continue;
+      o[i] = (uint32_t)((base + w.rows[r0 + r]) * 2 * COLS + c) * 4;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const float* q = red + ((t * 4 + c / kCols * SHARES) * 16 + r) * kCols + c % kCols;
-        v[t] = load4(q);
-#pragma unroll
-        for (int s = 1; s < SHARES; ++s) v[t] += load4(q + s * 16 * kCols);
+        const Val* q = red + (t * SHARES * 16 + r) * COLS + c;
+        v[i][t] = *reinterpret_cast<const Acc*>(q) +
+                  *reinterpret_cast<const Acc*>(q + 16 * COLS);
       }
-      float h[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = silu_f32(v[0][q]) * v[1][q];
-      // in bf16 rounded once, as the layer's h
-      store_n(reinterpret_cast<typename Kind<P>::T*>(hbuf + r * PITCH) + c, h);
     }
-    __syncthreads();
-    const char* hrow = hbuf + lr * PITCH + (lane >> 4) * 16;
-    const int g = lane >> 4, c = lane & 15;
-    for (int t = wave; t < tiles; t += kWaves) {
+    if (p.splits > 1) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = Acc{};
+      for (int i = 0; i < Q::N; ++i)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uint4 x[NX];
+        for (int t = 0; t < 2; ++t)
+          store_shared(part, o[i] + split * one + t * COLS * 4,
+                       __builtin_bit_cast(f32x4_t, v[i][t]));
+      stores_done();
+      if (tid == 0) w.count[0] = count_up(p.split_done + at * p.rounds + r0 / 16);
+      __syncthreads();
+      const bool last = uniform(w.count[0]) == p.splits - 1;
+      __syncthreads();
+      if (!last) continue;
 #pragma unroll
-        for (int i = 0; i < NX; ++i)
-          x[i] = *reinterpret_cast<const uint4*>(hrow + (ks * NX + i) * 64);
-        if (KS % 2 == 0) {
-          st[ks & 1].compute(x, acc);
-          load(st[ks & 1]);
-        } else {  // one step to a tile: the two in turn by moving
-          st[0].compute(x, acc);
-          st[0] = st[1];
-          load(st[1]);
+      for (int i = 0; i < Q::N; ++i) {
+        Acc q[kMaxSplits][2];
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            q[s][t] = __builtin_bit_cast(
+                Acc, load_shared(part, s < p.splits ? o[i] + s * one + t * COLS * 4 : kPastEnd));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          v[i][t] = q[0][t];
+#pragma unroll
+          for (int s = 1; s < kMaxSplits; ++s) v[i][t] += q[s][t];
         }
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 4 * g + r, col = t * kCols + 4 * c;
-        if (row >= rows || col >= p.H) continue;
-        const int at = (shared ? p.F : 0) + w.rows[r0 + row];
-        store_shared(y, (uint32_t)(at * p.H + col) * 4,
-                     f32x4_t{acc[0][r], acc[1][r], acc[2][r], acc[3][r]});
-      }
     }
-    if (r0 + 16 < n) __syncthreads();
-  }
-  // the last of the entry's column groups adds their rows, in order, into the first's
-  stores_done();
-  if (slices > 1) {
-    if (tid == 0) w.count[0] = count_up(p.entry_done + (shared ? p.entries : 0) + entry);
-    __syncthreads();
-    if (uniform(w.count[0]) != slices - 1) return;
-    const uint32_t one = (uint32_t)(p.F + p.S) * p.H * 4;
-    const rsrc_t all = make_rsrc(p.y, (int64_t)slices * one);
-    const int quads = p.H / 4;
-    for (int i = tid; i < n * quads; i += kThreads) {
-      const int r = i / quads, c = (i - r * quads) * 4;
-      const uint32_t o = (uint32_t)(((shared ? p.F : 0) + w.rows[r]) * p.H + c) * 4;
-      f32x4_t a = {0.f, 0.f, 0.f, 0.f};
-      for (int s0 = 0; s0 < slices; s0 += 8) {
-        f32x4_t v[8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          v[s] = load_shared(all, s0 + s < slices ? o + (s0 + s) * one : kPastEnd);
-#pragma unroll
-        for (int s = 0; s < 8; ++s) a += v[s];
-      }
-      store_shared(all, o, a);
-    }
-    stores_done();
-  }
-  combine(p, w);
-}
-
-// 8-bit weights, up and gate: workgroup (entry, 64 columns), 4 shares of K each.
-__global__ __launch_bounds__(kThreads, 4) void few_up_i8_kernel(FewArgs p) {
-  __shared__ __align__(16) int red[kWaves * 16 * kCols];
-  __shared__ uint32_t tops[16];
-  __shared__ Work w;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = uniform(tid >> 6);
-  const int64_t routed = (int64_t)p.entries * p.slices;
-  const bool shared = blockIdx.x >= routed;
-  const int slices = shared ? p.slices_s : p.slices;
-  const int b = shared ? (int)(blockIdx.x - routed) : (int)blockIdx.x;
-  const int entry = uniform(b / slices), slice = b - entry * slices;
-  if (!find_work(p, entry, shared, reinterpret_cast<float*>(red), w)) return;
-  const int n = uniform(w.n), e = shared ? 0 : uniform(w.expert);
-  const int D = shared ? p.Ds : p.D, d0 = slice * kCols;
-  const int64_t size = i8_matrix_bytes(p.H, D), scales = i8_code_bytes(p.H, D);
-  const char* const* mats = shared ? p.ws : p.w;
-  const Columns<kI8> m(mats[wave / 4] + e * size, p.H, D, d0);
-  float* out = shared ? p.h + (int64_t)p.F * p.D : p.h;
-  for (int r0 = 0; r0 < n; r0 += 16) {
-    const int rows = n - r0 < 16 ? n - r0 : 16;
-    const int lr = lane & 15, f = lr < rows ? w.rows[r0 + lr] : 0;
-    const Rows a = {make_rsrc(p.xc, (int64_t)p.S * p.H),
-                    lr < rows ? (uint32_t)(shared ? f : f / p.k) * p.H : kPastEnd, (uint32_t)p.H};
-    if (tid < 16) tops[tid] = 0;
-    i32x4_t acc[4];
-    stream<kI8>(m, a, wave % 4, 4, (int)i8_tiles_k(p.H), acc);
-    put_sums<kI8>(acc, red + wave * 16 * kCols, rows);
-    __syncthreads();
-    const int r = tid / 16, c = tid % 16 * 4;
-    if (r < rows && d0 + c < D) {
-      i32x4_t v[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int* q = red + (t * 4 * 16 + r) * kCols + c;
-        v[t] = *reinterpret_cast<const i32x4_t*>(q);
-#pragma unroll
-        for (int s = 1; s < 4; ++s) v[t] += *reinterpret_cast<const i32x4_t*>(q + s * 16 * kCols);
-      }
+    for (int i = 0; i < Q::N; ++i) {
+      const int r = r1 + i * Q::STRIDE;
+      if (r >= rows || d0 + c >= D) continue;
       const int row = w.rows[r0 + r];
-      const float x = p.xs[shared ? row : row / p.k];
-      const f32x4_t su = load4(reinterpret_cast<const float*>(mats[0] + e * size + scales) + d0 + c);
-      const f32x4_t sg = load4(reinterpret_cast<const float*>(mats[1] + e * size + scales) + d0 + c);
-      float h[4];
-      uint32_t top = 0;
+      float u[4], g[4], hv[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        h[q] = silu_f32((float)v[0][q] * x * su[q]) * ((float)v[1][q] * x * sg[q]);
-        const uint32_t bits = abs_bits(h[q]);
-        top = top > bits ? top : bits;
+      for (int q = 0; q < 4; ++q) u[q] = (float)v[i][0][q], g[q] = (float)v[i][1][q];
+      if constexpr (I8) {
+        const float x = p.xs[shared ? row : row / p.k];
+        const int64_t sc = e * size + i8_code_bytes(p.H, D);
+        const f32x4_t su = load4(reinterpret_cast<const float*>(mats[0] + sc) + d0 + c);
+        const f32x4_t sg = load4(reinterpret_cast<const float*>(mats[1] + sc) + d0 + c);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u[q] = u[q] * x * su[q], g[q] = g[q] * x * sg[q];
       }
-      store_n(out + (int64_t)row * D + d0 + c, h);
-      atomicMax(&tops[r], top);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) hv[q] = silu_f32(u[q]) * g[q];
+      const int64_t to = (int64_t)row * D + d0 + c;
+      if constexpr (P == kBf16)  // rounded once, as the layer's h
+        store_n(reinterpret_cast<bf16_t*>(p.h) + (shared ? (int64_t)p.F * p.D : 0) + to, hv);
+      else
+        store_shared(h, (uint32_t)to * 4, f32x4_t{hv[0], hv[1], hv[2], hv[3]});
     }
-    __syncthreads();
-    if (tid < rows)
-      atomicMax(p.top + (shared ? p.F : 0) + w.rows[r0 + tid], tops[tid]);
+    if constexpr (I8) {
+      // the entry's last column group: codes of its rows
+      stores_done();
+      if (tid == 0) w.count[0] = count_up(p.entry_done + (shared ? p.entries : 0) + entry);
+      __syncthreads();
+      const bool last = uniform(w.count[0]) == slices * ((n + 15) / 16) - 1;
+      __syncthreads();
+      if (last)
+        for (int r = wave; r < n; r += 4) {
+          const int row = w.rows[r];
+          quantize_row(h, (uint32_t)row * D * 4, D,
+                       p.hc + (shared ? (int64_t)p.F * p.D : 0) + (int64_t)row * D,
+                       p.hs + base + row);
+        }
+    } else if (r0 + 16 < n) {
+      __syncthreads();
+    }
   }
 }
 
-// 8-bit weights, down: workgroup (entry, 128 columns of H), 2 x 4 shares of D; h's rows are
-// quantised on their way.
-__global__ __launch_bounds__(kThreads, 4) void few_down_i8_kernel(FewArgs p, int groups) {
-  __shared__ __align__(16) int red[kWaves * 16 * kCols];
+// Workgroup (entry, CT column tiles of H): waves CT x 4 / CT shares of D.
+template <int P, int CT>
+__global__ __launch_bounds__(kExpertThreads, 2) void few_down_kernel(FewArgs p) {
+  using Val = typename Kind<P>::Val;
+  using Acc = typename Kind<P>::Acc;
+  using Q = Quads<P>;
+  constexpr bool I8 = P == kI8;
+  constexpr int COLS = Kind<P>::COLS, STEP = Kind<P>::STEP, SHARES = 4 / CT;
+  constexpr int HS = P == kBf16 ? 2 : P == kF32 ? 4 : 1;  // bytes of the operand
+  __shared__ __align__(16) Val red[4 * 16 * COLS];
   __shared__ Work w;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
-  const int all = uniform((int)blockIdx.x / groups), group = blockIdx.x - all * groups;
+  const int all = uniform((int)blockIdx.x / p.cols), group = blockIdx.x - all * p.cols;
   const bool shared = all >= p.entries;
   const int entry = shared ? all - p.entries : all;
-  if (!find_work(p, entry, shared, nullptr, w)) return;
+  if (!find_work<kExpertThreads>(p, entry, shared, nullptr, w)) return;
   const int n = uniform(w.n), e = shared ? 0 : uniform(w.expert);
-  const int D = shared ? p.Ds : p.D;
-  const char* matrix = (shared ? p.ws[2] : p.w[2]) + e * i8_matrix_bytes(D, p.H);
-  const int n0 = group * 2 * kCols;
-  const Columns<kI8> m(matrix, D, p.H, n0 + wave / 4 * kCols);
-  const int steps = (int)i8_tiles_k(D);
-  const uint32_t* tops = p.top + (shared ? p.F : 0);
-  const float* in = shared ? p.h + (int64_t)p.F * p.D : p.h;
-  const rsrc_t y = make_rsrc(p.y + (shared ? (int64_t)p.F * p.H : 0),
-                             (int64_t)(shared ? p.S : p.F) * p.H * 4);
+  const int D = shared ? p.Ds : p.D, base = shared ? p.F : 0;
+  const int64_t size = I8 ? i8_matrix_bytes(D, p.H) : (int64_t)D * p.H * Kind<P>::ES;
+  const char* matrix = (shared ? p.ws[2] : p.w[2]) + e * size;
+  const int n0 = group * CT * COLS;
+  Columns<P> m(matrix, D, p.H, n0 + wave / SHARES * COLS);
+  const int steps = (D + STEP - 1) / STEP;
+  const char* in = (I8 ? (const char*)p.hc : p.h) + (shared ? (int64_t)p.F * p.D * HS : 0);
+  const uint32_t bytes = (uint32_t)D * HS;
+  const rsrc_t y = make_rsrc(p.y, (int64_t)(p.F + p.S) * p.H * 4);
   for (int r0 = 0; r0 < n; r0 += 16) {
     const int rows = n - r0 < 16 ? n - r0 : 16;
     const int lr = lane & 15, f = lr < rows ? w.rows[r0 + lr] : 0;
-    const uint32_t bytes = (uint32_t)D * 4;
-    const QuantRows a = {make_rsrc(in, (int64_t)(shared ? p.S : p.F) * bytes),
-                         lr < rows ? f * bytes : kPastEnd, bytes, Quant(lr < rows ? tops[f] : 0)};
-    constexpr int DEPTH = 2;
-    Step<kI8> st[DEPTH];
-    QuantRows::Raw x[DEPTH];
-    const int first = wave % 4;
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      st[d].load(m, first + d * 4, steps);
-      a.load(first + d * 4, x[d]);
-    }
-    i32x4_t acc[4] = {};
-    for (int s = first; s < steps;) {
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d, s += 4) {
-        uint4 codes[1];
-        a.codes(x[d], codes);
-        st[d].compute(codes, acc);
-        st[d].load(m, s + DEPTH * 4, steps);
-        a.load(s + DEPTH * 4, x[d]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    put_sums<kI8>(acc, red + wave * 16 * kCols, rows);
+    const Rows a = {make_rsrc(in, (int64_t)(shared ? p.S : p.F) * bytes),
+                    lr < rows ? f * bytes : kPastEnd, bytes};
+    asm volatile("" : "+v"(m.off));
+    Acc acc[Step<P>::NJ];
+    stream<P, SHARES, 3>(m, a, wave % SHARES, steps, acc);
+    put_sums<P>(acc, red + wave * 16 * COLS, rows);
     __syncthreads();
-    const int half = tid / 256, r = tid / 16 % 16, c = tid % 16 * 4;
-    const int col = n0 + half * kCols + c;
-    if (r < rows && col < p.H) {
-      const int* q = red + (half * 4 * 16 + r) * kCols + c;
-      i32x4_t v = *reinterpret_cast<const i32x4_t*>(q);
+    for (int i = tid; i < rows * CT * Q::PER_ROW; i += kExpertThreads) {
+      const int r = i / (CT * Q::PER_ROW), tile = i / Q::PER_ROW % CT, c = i % Q::PER_ROW * 4;
+      const int col = n0 + tile * COLS + c;
+      if (col >= p.H) continue;
+      const Val* q = red + (tile * SHARES * 16 + r) * COLS + c;
+      Acc v = *reinterpret_cast<const Acc*>(q);
 #pragma unroll
-      for (int s = 1; s < 4; ++s) v += *reinterpret_cast<const i32x4_t*>(q + s * 16 * kCols);
-      const int row = w.rows[r0 + r];
-      const float xs = Quant(tops[row]).scale;
-      const f32x4_t sw = load4(reinterpret_cast<const float*>(matrix + i8_code_bytes(D, p.H)) + col);
+      for (int s = 1; s < SHARES; ++s) v += *reinterpret_cast<const Acc*>(q + s * 16 * COLS);
+      const int row = base + w.rows[r0 + r];
       f32x4_t o;
+      if constexpr (I8) {
+        const float hs = p.hs[row];
+        const f32x4_t sw =
+            load4(reinterpret_cast<const float*>(matrix + i8_code_bytes(D, p.H)) + col);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = (float)v[i] * xs * sw[i];
+        for (int q = 0; q < 4; ++q) o[q] = (float)v[q] * hs * sw[q];
+      } else {
+        o = v;
+      }
       store_shared(y, (uint32_t)(row * p.H + col) * 4, o);
     }
     if (r0 + 16 < n) __syncthreads();
   }
   stores_done();
-  if (groups > 1) {
-    if (tid == 0) w.count[0] = count_up(p.entry_done + (shared ? p.entries : 0) + entry);
-    __syncthreads();
-    if (uniform(w.count[0]) != groups - 1) return;
-  }
-  combine(p, w);
+  combine<kExpertThreads>(p, w, group, n0, CT * COLS);
 }
 
 // ------------------------------------------------------------ host
@@ -890,59 +831,74 @@ moe_status check_few(const moe_shape* s, bool i8) {
   const int64_t widest = s->D > s->D_shared ? s->D : s->D_shared;
   const int64_t es = i8 ? 1 : s->dtype == MOE_F32 ? 4 : 2;
   if ((s->H + 64) * (widest + 64) * es >= kMaxMatrix) return MOE_ERR_UNSUPPORTED;
-  // the column groups' rows of y, addressed from one base
-  const int64_t groups = i8 ? 1 : (widest + kCols - 1) / kCols;
-  if (groups * (s->S * s->k + s->S) * s->H * 4 >= kMaxMatrix) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
-// Columns of D to a workgroup: 64 while there are few (at one token every workgroup counts),
-// 128 beyond.
-int column_group(const moe_shape* s) { return s->S * s->k >= 256 ? 2 : 1; }
-
 struct FewWs {
-  size_t words, score, xc, xs, h, y, total;
-  int entries, by_row, shared, slices, slices_s, route_splits;
-  int token_done, top, n_words;  // ints from words on
+  size_t words, score, xc, xs, h, hc, hs, part, y, total;
+  int entries, by_row, shared, slices, slices_s, splits, rounds, route_splits, tiles, cols;
+  int split_done, token_done, n_words;  // ints from words on
 };
 FewWs few_ws(const moe_shape* s, bool i8) {
   FewWs w = {};
   const int64_t F = s->S * s->k;
   auto up = [](int64_t a, int64_t b) { return (int)((a + b - 1) / b); };
+  const int cols = i8 ? kCols8 : kCols;
   w.by_row = F <= s->E;
   w.entries = (int)(w.by_row ? F : s->E);
   w.shared = s->D_shared ? up(s->S, 16) : 0;
-  const int cols = i8 ? kCols : column_group(s) * kCols;
   w.slices = up(s->D, cols);
   w.slices_s = s->D_shared ? up(s->D_shared, cols) : 0;
   w.route_splits = up(s->H, kRouteRows);
-  w.token_done = w.entries + w.shared;
-  w.top = w.token_done + (int)s->S;
-  w.n_words = w.top + (i8 ? (int)(F + s->S) : 0);
+  // H in parts where there are not enough column groups for the CUs; few assignments, since
+  // each part keeps its sums of every one
+  const int groups = w.entries * w.slices + w.shared * w.slices_s;
+  w.splits = 1;
+  if (F <= kSplitRows && groups > 0) {
+    w.splits = kWanted / groups;
+    const int most = up(s->H, 2 * 64);  // two steps of bf16 for each wave
+    if (w.splits > most) w.splits = most;
+    if (w.splits > kMaxSplits) w.splits = kMaxSplits;
+    if (w.splits < 1) w.splits = 1;
+  }
+  w.rounds = up(F > s->S ? F : s->S, 16);
+  // two column tiles of H to a workgroup where that leaves enough of them
+  w.tiles = (w.entries + w.shared) * up(s->H, 2 * cols) >= 2 * kWanted ? 2 : 1;
+  w.cols = up(s->H, w.tiles * cols);
+  w.split_done = w.entries + w.shared;
+  w.token_done = w.split_done + (w.splits > 1 ? groups * w.rounds : 0);
+  w.n_words = w.token_done + (int)s->S * w.cols;
   size_t o = 0;
   auto take = [&](size_t n) {
     const size_t at = o;
     o += ffn_round_up(n, 256);
     return at;
   };
-  const int most = w.slices > w.slices_s ? w.slices : w.slices_s;
+  const size_t n_h = (size_t)(F * s->D + s->S * s->D_shared);
   w.words = take((size_t)w.n_words * 4);
   w.score = take((size_t)w.route_splits * s->S * s->E * 4);
   w.xc = take(i8 ? (size_t)s->S * s->H : 0);
   w.xs = take(i8 ? (size_t)s->S * 4 : 0);
-  w.h = take(i8 ? (size_t)(F * s->D + s->S * s->D_shared) * 4 : 0);
-  w.y = take((size_t)(i8 ? 1 : most) * (F + s->S) * s->H * 4);
+  w.h = take(n_h * (!i8 && s->dtype == MOE_BF16 ? 2 : 4));
+  w.hc = take(i8 ? n_h : 0);
+  w.hs = take(i8 ? (size_t)(F + s->S) * 4 : 0);
+  w.part = take(w.splits > 1 ? (size_t)groups * w.splits * (F + s->S) * 2 * cols * 4 : 0);
+  w.y = take((size_t)(F + s->S) * s->H * 4);
   w.total = o ? o : 256;
   return w;
 }
 
 template <int P>
-void launch_experts(const FewArgs& p, int cg, hipStream_t st) {
-  const unsigned grid = (unsigned)(p.entries * p.slices + p.shared * p.slices_s);
-  if (cg == 1)
-    few_expert_kernel<P, 1><<<grid, kThreads, 0, st>>>(p);
+void launch_experts(const FewArgs& p, int tiles, hipStream_t st) {
+  const unsigned groups = (unsigned)(p.entries * p.slices + p.shared * p.slices_s);
+  few_up_kernel<P><<<groups * p.splits, kExpertThreads, 0, st>>>(p);
+  FewArgs d = p;
+  d.routed = 1;
+  const unsigned grid = (unsigned)((p.entries + p.shared) * p.cols);
+  if (tiles == 1)
+    few_down_kernel<P, 1><<<grid, kExpertThreads, 0, st>>>(d);
   else
-    few_expert_kernel<P, 2><<<grid, kThreads, 0, st>>>(p);
+    few_down_kernel<P, 2><<<grid, kExpertThreads, 0, st>>>(d);
 }
 
 template <int R>
@@ -1000,12 +956,15 @@ moe_status few_forward(const moe_shape* s, bool i8, const void* A, const void* W
   p.O = O;
   p.score = (float*)(ws + z.score);
   p.entry_done = (int*)(ws + z.words);
+  p.split_done = p.entry_done + z.split_done;
   p.token_done = p.entry_done + z.token_done;
-  p.top = (uint32_t*)(p.entry_done + z.top);
   p.n_words = z.n_words;
   p.xc = (int8_t*)(ws + z.xc);
   p.xs = (float*)(ws + z.xs);
-  p.h = (float*)(ws + z.h);
+  p.h = ws + z.h;
+  p.hc = (int8_t*)(ws + z.hc);
+  p.hs = (float*)(ws + z.hs);
+  p.part = ws + z.part;
   p.y = (float*)(ws + z.y);
   p.S = (int)s->S;
   p.H = (int)s->H;
@@ -1019,6 +978,9 @@ moe_status few_forward(const moe_shape* s, bool i8, const void* A, const void* W
   p.shared = z.shared;
   p.slices = z.slices;
   p.slices_s = z.slices_s;
+  p.splits = z.splits;
+  p.rounds = z.rounds;
+  p.cols = z.cols;
   p.route_splits = z.route_splits;
   p.renormalize = s->renormalize;
   p.out_f32 = s->dtype == MOE_F32 || (s->flags & MOE_OUTPUT_F32) != 0;
@@ -1031,18 +993,12 @@ moe_status few_forward(const moe_shape* s, bool i8, const void* A, const void* W
     few_topk_kernel<<<(unsigned)p.S, 256, 0, st>>>(p);
     p.routed = 1;
   }
-  if (i8) {
-    few_up_i8_kernel<<<(unsigned)(p.entries * p.slices + p.shared * p.slices_s), kThreads, 0,
-                       st>>>(p);
-    p.routed = 1;
-    const int groups = (p.H + 2 * kCols - 1) / (2 * kCols);
-    few_down_i8_kernel<<<(unsigned)((p.entries + p.shared) * groups), kThreads, 0, st>>>(p,
-                                                                                         groups);
-  } else if (s->dtype == MOE_F32) {
-    launch_experts<kF32>(p, column_group(s), st);
-  } else {
-    launch_experts<kBf16>(p, column_group(s), st);
-  }
+  if (i8)
+    launch_experts<kI8>(p, z.tiles, st);
+  else if (s->dtype == MOE_F32)
+    launch_experts<kF32>(p, z.tiles, st);
+  else
+    launch_experts<kBf16>(p, z.tiles, st);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
