@@ -29,7 +29,7 @@
 //   bf16: a lane holds 8 rows of 8 columns; byte permutes give the operands (8 rows of a
 //         column) of v_mfma_f32_16x16x32_bf16
 //   fp32: 4 rows of 2 x 4 columns, v_mfma_f32_16x16x4_f32 (K in an order that suits)
-//   int8: packed in operand order, 64 columns, v_mfma_i32_16x16x64_i8; h's row scale needs the
+//   int8: packed in operand order, v_mfma_i32_16x16x64_i8; h's row scale needs the
 //         whole row: the last of an entry's workgroups quantises its rows
 #include "gemm_direct.h"
 #include "i8.h"
@@ -48,10 +48,8 @@ constexpr int kMaxRows = (int)kMaxTokens * 32;  // assignments
 constexpr int kThreads = 512, kWaves = 8;  // router
 constexpr int kExpertThreads = 256;
 constexpr int kCols = 128;           // columns of a wave
-constexpr int kCols8 = 64;           // with 8-bit weights
 constexpr int kMaxSplits = 8;        // parts of H
 constexpr int kWanted = 512;         // workgroups: as many as the chip holds
-constexpr int kSplitRows = 64;       // assignments up to which it is cut
 constexpr int kRouteRows = 512;      // K rows of a router workgroup, 64 to a wave
 constexpr int kOwnRoute = 8;         // tokens that each workgroup routes for itself
 
@@ -66,7 +64,7 @@ struct FewArgs {
   void* O;
   float* score;        // [route splits][S][E]
   int* entry_done;     // [entries + shared] int8: arrived column groups of each 16 rows
-  int* split_done;     // [column groups][rounds of 16 rows] arrived parts of H
+  int* split_done;     // [column groups of D][rounds] arrived parts of H
   int* token_done;     // [S][column groups of H] arrived entries
   int n_words;         // of these
   int8_t* xc;          // int8: codes and scales of the tokens
@@ -74,13 +72,14 @@ struct FewArgs {
   char* h;             // [F][D], then [S][Ds] (fp32 with 8-bit weights)
   int8_t* hc;          // int8: its codes and scales
   float* hs;
-  char* part;          // [column groups][splits][F + S][2][columns]
+  char* part;          // [splits][F + S][2][D or Ds]
   float* y;            // [F + S][H]
   int S, H, D, Ds, E, k, F;
   int by_row, entries; // an entry per assignment (the first of its expert), or per expert
   int shared;          // shared entries
   int slices, slices_s;  // column groups of D
   int splits, rounds;  // parts of H; rounds of 16 rows at most
+  int blocks;          // workgroups that share an entry's rounds
   int cols;            // column groups of H
   int route_splits, renormalize, out_f32;
   int routed;          // ids and tw are there (given, or by a launch before)
@@ -133,21 +132,21 @@ struct Kind<kBf16> {
   using T = bf16_t;     // activations
   using Val = float;
   using Acc = f32x4_t;
-  static constexpr int ES = 2, STEP = 32, COLS = kCols;  // bytes of a weight, K per step
+  static constexpr int ES = 2, STEP = 32;  // bytes of a weight, K per step
 };
 template <>
 struct Kind<kF32> {
   using T = float;
   using Val = float;
   using Acc = f32x4_t;
-  static constexpr int ES = 4, STEP = 16, COLS = kCols;
+  static constexpr int ES = 4, STEP = 16;
 };
 template <>
 struct Kind<kI8> {
   using T = bf16_t;
   using Val = int;
   using Acc = i32x4_t;
-  static constexpr int ES = 1, STEP = 64, COLS = kCols8;
+  static constexpr int ES = 1, STEP = 64;
 };
 
 // A wave's columns of a matrix [K][N] from n0 on, K values from k0 on.
@@ -185,12 +184,11 @@ struct Columns {
 template <int P>
 struct Step {
   using Acc = typename Kind<P>::Acc;
-  static constexpr int NJ = P == kI8 ? 4 : 8;  // loads, and accumulators
-  uint4 w[NJ];
+  uint4 w[8];
 
   __device__ __forceinline__ void load(const Columns<P>& m, uint32_t o) {
 #pragma unroll
-    for (int i = 0; i < NJ; ++i) {
+    for (int i = 0; i < 8; ++i) {
       uint32_t at = o + i * m.row;
       if constexpr (P == kF32) at = (o + (i >> 1) * m.row + (i & 1) * 256) | m.past[i & 1];
       w[i] = __builtin_bit_cast(
@@ -201,7 +199,7 @@ struct Step {
   __device__ __forceinline__ void load(const Columns<P>& m, int s, int end) {
     load(m, s < end ? m.off + (uint32_t)s * m.step : kPastEnd);
   }
-  __device__ __forceinline__ void compute(const uint4& x, Acc (&acc)[NJ]) const {
+  __device__ __forceinline__ void compute(const uint4& x, Acc (&acc)[8]) const {
     if constexpr (P == kBf16) {
       const bf16x8_t a = __builtin_bit_cast(bf16x8_t, x);
 #pragma unroll
@@ -226,7 +224,7 @@ struct Step {
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 8; ++j)
         acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, x),
                                                        __builtin_bit_cast(i32x4_t, w[j]), acc[j],
                                                        0, 0, 0);
@@ -248,17 +246,17 @@ struct Rows {
 };
 // This lane's sums into LDS as rows of the wave's columns: rows 4 (l / 16) .. + 3 below n.
 template <int P>
-__device__ __forceinline__ void put_sums(const typename Kind<P>::Acc (&acc)[Step<P>::NJ],
+__device__ __forceinline__ void put_sums(const typename Kind<P>::Acc (&acc)[8],
                                          typename Kind<P>::Val* to, int n) {
   using Acc = typename Kind<P>::Acc;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (4 * g + r >= n) continue;
-    typename Kind<P>::Val* row = to + (4 * g + r) * Kind<P>::COLS;
+    typename Kind<P>::Val* row = to + (4 * g + r) * kCols;
     if constexpr (P == kI8) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) row[16 * j + c] = acc[j][r];
+      for (int j = 0; j < 8; ++j) row[16 * j + c] = acc[j][r];
     } else {
       const int at0 = P == kBf16 ? 8 * c : 4 * c, at1 = P == kBf16 ? 8 * c + 4 : 64 + 4 * c;
       *reinterpret_cast<Acc*>(row + at0) = Acc{acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
@@ -426,7 +424,8 @@ __global__ __launch_bounds__(256) void few_topk_kernel(FewArgs p) {
 struct Work {
   int n;           // rows
   int expert;      // -1: shared
-  int count[2];
+  int count;
+  int part[8], first[8];
   int done[64];    // tokens complete
   uint16_t rows[kMaxRows];       // assignments (shared: tokens)
   int ids[kOwnRoute * 32];       // of the tokens that this workgroup has routed for itself
@@ -438,21 +437,24 @@ struct Work {
 template <int THREADS>
 __device__ __forceinline__ bool find_work(const FewArgs& p, int y, bool shared, float* lds,
                                           Work& w) {
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   if (!p.routed) {
     sum_scores(p, 0, p.S, tid, THREADS, lds);
     __syncthreads();
-    for (int t = uniform(tid >> 6); t < p.S; t += THREADS / 64)
-      topk_one(lds + t * p.E, p.E, p.k, p.renormalize, w.ids + t * p.k, w.tw + t * p.k, tid & 63);
-    __syncthreads();
-    if (blockIdx.x == 0 && tid < p.F) {
-      p.ids[tid] = w.ids[tid];
-      p.tw[tid] = w.tw[tid];
+    for (int t = wave; t < p.S; t += THREADS / 64) {
+      float score, top;
+      int id;
+      topk_select(lds + t * p.E, p.E, p.k, lane, score, id, top);
+      if (lane < p.k) w.ids[t * p.k + lane] = id;
     }
+    __syncthreads();
+    if (blockIdx.x == 0)  // the weights are the next launch's
+      for (int t = wave; t < p.S; t += THREADS / 64)
+        topk_one(lds + t * p.E, p.E, p.k, p.renormalize, p.ids + t * p.k, p.tw + t * p.k, lane);
   } else if (p.F <= kOwnRoute * 32) {
-    if (tid < p.F) {
-      w.ids[tid] = p.ids[tid];
-      w.tw[tid] = p.tw[tid];
+    for (int f = tid; f < p.F; f += THREADS) {
+      w.ids[f] = p.ids[f];
+      w.tw[f] = p.tw[f];
     }
     __syncthreads();
   }
@@ -469,31 +471,44 @@ __device__ __forceinline__ bool find_work(const FewArgs& p, int y, bool shared, 
   const bool here = p.F <= kOwnRoute * 32;
   const int e = uniform(!p.by_row ? y : here ? w.ids[y] : p.ids[y]);
   if (e < 0 || e >= p.E) return false;
-  if (tid == 0) w.count[0] = w.count[1] = 0;
-  __syncthreads();
-  if (here) {
-    // in their order: workgroups that share the rows' sums list them alike
-    if (tid < p.F && w.ids[tid] == e) {
-      int at = 0;
-      for (int f = 0; f < tid; ++f) at += w.ids[f] == e;
-      w.rows[at] = (uint16_t)tid;
-      if (p.by_row && tid < y) w.count[1] = 1;  // an earlier entry's
-      atomicAdd(&w.count[0], 1);
-    }
-  } else {
-    // in no particular order: rows do not meet in the products
-    for (int f = tid; f < p.F; f += THREADS)
-      if (p.ids[f] == e) {
-        if (p.by_row && f < y) w.count[1] = 1;
-        w.rows[atomicAdd(&w.count[0], 1)] = (uint16_t)f;
-      }
+  // each wave a stretch of the assignments, in their order: workgroups that share the rows
+  // list them alike
+  const int per = (p.F + THREADS - 1) / THREADS * 64, f0 = wave * per;
+  const int f1 = f0 + per < p.F ? f0 + per : p.F;
+  auto mine = [&](int f) { return f < f1 && (here ? w.ids[f] : p.ids[f]) == e; };
+  int n = 0, first = p.F;
+  for (int f = f0; f < f1; f += 64) {
+    const uint64_t b = __ballot(mine(f + lane));
+    if (n == 0 && b != 0) first = f + (int)__builtin_ctzll(b);
+    n += (int)__popcll(b);
   }
-  if (tid == 0) w.expert = e;
+  if (lane == 0) {
+    w.part[wave] = n;
+    w.first[wave] = first;
+  }
   __syncthreads();
-  if (tid == 0) w.n = w.count[0];
-  const bool mine = uniform(w.count[1]) == 0 && uniform(w.count[0]) > 0;
+  int at = 0, all = 0;
+  first = p.F;
+#pragma unroll
+  for (int i = 0; i < THREADS / 64; ++i) {
+    if (i < wave) at += w.part[i];
+    all += w.part[i];
+    first = first < w.first[i] ? first : w.first[i];
+  }
+  if (uniform(all) == 0 || (p.by_row && uniform(first) != y)) return false;  // an earlier entry's
+  if (n > 0)
+    for (int f = f0; f < f1; f += 64) {
+      const bool m = mine(f + lane);
+      const uint64_t b = __ballot(m);
+      if (m) w.rows[at + __popcll(b & ((1ull << lane) - 1))] = (uint16_t)(f + lane);
+      at += (int)__popcll(b);
+    }
+  if (tid == 0) {
+    w.n = all;
+    w.expert = e;
+  }
   __syncthreads();
-  return mine;
+  return true;
 }
 
 __device__ __forceinline__ bool valid_slot(const FewArgs& p, const Work& w, int f) {
@@ -504,18 +519,21 @@ __device__ __forceinline__ bool valid_slot(const FewArgs& p, const Work& w, int 
 // The tokens whose columns n0 .. + width - 1 this workgroup completes: O_t = sum_j w_tj y_tj (+
 // the shared row), slots without an expert left out. Its own rows of y are in memory.
 template <int THREADS>
-__device__ __forceinline__ void combine(const FewArgs& p, Work& w, int group, int n0, int width) {
+__device__ __forceinline__ void combine(const FewArgs& p, Work& w, int block, int blocks, int group,
+                                        int n0, int width) {
   const int tid = threadIdx.x;
   const int n = uniform(w.n);
   const bool shared = uniform(w.expert) < 0;
   const rsrc_t y = make_rsrc(p.y, (int64_t)(p.F + p.S) * p.H * 4);
   const int quads = (p.H - n0 < width ? p.H - n0 : width) / 4;
-  for (int r0 = 0; r0 < n; r0 += 64) {
+  // 4 of this workgroup's rounds at a time
+  for (int r0 = 16 * block; r0 < n; r0 += 64 * blocks) {
     if (tid < 64) {
       bool last = false;
       int tok = 0;
-      if (r0 + tid < n) {
-        const int f = w.rows[r0 + tid];
+      const int r = r0 + tid / 16 * 16 * blocks + tid % 16;
+      if (r < n) {
+        const int f = w.rows[r];
         tok = shared ? f : f / p.k;
         int need = p.shared ? 1 : 0;
         for (int j = 0; j < p.k; ++j) need += valid_slot(p, w, tok * p.k + j);
@@ -523,10 +541,10 @@ __device__ __forceinline__ void combine(const FewArgs& p, Work& w, int group, in
       }
       const uint64_t b = __ballot(last);
       if (last) w.done[__popcll(b & ((1ull << tid) - 1))] = tok;
-      if (tid == 0) w.count[0] = __popcll(b);
+      if (tid == 0) w.count = __popcll(b);
     }
     __syncthreads();
-    const int all = uniform(w.count[0]) * quads;
+    const int all = uniform(w.count) * quads;
     for (int i = tid; i < all; i += THREADS) {
       const int d = i / quads, c = n0 + (i - d * quads) * 4, t = w.done[d];
       f32x4_t a = {0.f, 0.f, 0.f, 0.f};
@@ -564,7 +582,7 @@ __device__ __forceinline__ void combine(const FewArgs& p, Work& w, int group, in
 // This wave's share of K's steps below `end`: every SHARES-th from `first` on.
 template <int P, int SHARES, int DEPTH>
 __device__ __forceinline__ void stream(const Columns<P>& m, const Rows& a, int first, int end,
-                                       typename Kind<P>::Acc (&acc)[Step<P>::NJ]) {
+                                       typename Kind<P>::Acc (&acc)[8]) {
   Step<P> st[DEPTH];
   uint4 x[DEPTH];
 #pragma unroll
@@ -573,7 +591,7 @@ __device__ __forceinline__ void stream(const Columns<P>& m, const Rows& a, int f
     x[d] = a.load(first + d * SHARES, end);
   }
 #pragma unroll
-  for (int j = 0; j < Step<P>::NJ; ++j) acc[j] = typename Kind<P>::Acc{};
+  for (int j = 0; j < 8; ++j) acc[j] = typename Kind<P>::Acc{};
   for (int s = first; s < end;) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d, s += SHARES) {
@@ -584,13 +602,6 @@ __device__ __forceinline__ void stream(const Columns<P>& m, const Rows& a, int f
     }
   }
 }
-
-// A thread's 4 columns of one or two rows of a round, and their places: rows r1 + i STRIDE.
-template <int P>
-struct Quads {
-  static constexpr int PER_ROW = Kind<P>::COLS / 4;
-  static constexpr int N = 16 * PER_ROW / kExpertThreads, STRIDE = 16 / N;
-};
 
 // Row f's codes and scale from its fp32 values, by one wave (twice read).
 __device__ __forceinline__ void quantize_row(rsrc_t h, uint32_t row, int D, int8_t* codes,
@@ -618,20 +629,24 @@ template <int P>
 __global__ __launch_bounds__(kExpertThreads, 2) void few_up_kernel(FewArgs p) {
   using Val = typename Kind<P>::Val;
   using Acc = typename Kind<P>::Acc;
-  using Q = Quads<P>;
   constexpr bool I8 = P == kI8;
-  constexpr int COLS = Kind<P>::COLS, STEP = Kind<P>::STEP;
-  constexpr int SHARES = 2, HS = P == kBf16 ? 2 : 4;
+  // a thread's 4 columns of two rows of a round: rows r1 and r1 + STRIDE
+  constexpr int PER_ROW = kCols / 4, N = 16 * PER_ROW / kExpertThreads, STRIDE = 16 / N;
+  constexpr int STEP = Kind<P>::STEP, SHARES = 2, HS = P == kBf16 ? 2 : 4;
   __shared__ __align__(16) Val red[4 * 16 * kCols];
   __shared__ Work w;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
-  const int64_t routed = (int64_t)p.entries * p.slices * p.splits;
+  // blocks of an entry's rounds (the shared expert's have one) outermost, then entries, their
+  // column groups, parts of H
+  const int64_t routed = (int64_t)p.blocks * p.entries * p.slices * p.splits;
   const bool shared = blockIdx.x >= routed;
   const int slices = shared ? p.slices_s : p.slices;
   const int b = shared ? (int)(blockIdx.x - routed) : (int)blockIdx.x;
-  const int group = uniform(b / p.splits), split = b - group * p.splits;
-  const int entry = uniform(group / slices), d0 = (group - entry * slices) * COLS;
+  const int g0 = uniform(b / p.splits), split = b - g0 * p.splits;
+  const int e0 = uniform(g0 / slices), d0 = (g0 - e0 * slices) * kCols;
+  const int block = shared ? 0 : uniform(e0 / p.entries), entry = e0 - block * p.entries;
+  const int blocks = shared ? 1 : p.blocks;
   if (!find_work<kExpertThreads>(p, entry, shared, reinterpret_cast<float*>(red), w)) return;
   const int n = uniform(w.n), e = shared ? 0 : uniform(w.expert);
   const int D = shared ? p.Ds : p.D;
@@ -640,62 +655,65 @@ __global__ __launch_bounds__(kExpertThreads, 2) void few_up_kernel(FewArgs p) {
   const int steps = (p.H + STEP - 1) / STEP, per = uniform((steps + p.splits - 1) / p.splits);
   const int end = (split + 1) * per < steps ? (split + 1) * per : steps;
   Columns<P> m(mats[wave / SHARES] + e * size, p.H, D, d0);
-  const int base = shared ? p.F : 0, at = shared ? p.entries * p.slices + group : group;
+  const int base = shared ? p.F : 0;
+  const int at = shared ? p.entries * p.slices + g0 : g0 - block * p.entries * p.slices;
   const rsrc_t h = make_rsrc(p.h + (shared ? (int64_t)p.F * p.D * HS : 0),
                              (int64_t)(shared ? p.S : p.F) * D * HS);
-  const uint32_t one = (uint32_t)(p.F + p.S) * 2 * COLS * 4;
-  const rsrc_t part = make_rsrc(p.part + (int64_t)at * p.splits * one, (int64_t)p.splits * one);
-  const int r1 = tid / Q::PER_ROW, c = tid % Q::PER_ROW * 4;
-  for (int r0 = 0; r0 < n; r0 += 16) {
+  // the shared expert's rows of sums behind the others'
+  const int64_t routed_part = (int64_t)p.splits * p.F * 2 * p.D * 4;
+  const uint32_t one = (uint32_t)(shared ? p.S : p.F) * 2 * D * 4;
+  const rsrc_t part = make_rsrc(p.part + (shared ? routed_part : 0), (int64_t)p.splits * one);
+  const int r1 = tid / PER_ROW, c = tid % PER_ROW * 4;
+  for (int r0 = 16 * block; r0 < n; r0 += 16 * blocks) {
     const int rows = n - r0 < 16 ? n - r0 : 16;
     const int lr = lane & 15, f = lr < rows ? w.rows[r0 + lr] : 0;
     const uint32_t bytes = (uint32_t)p.H * Kind<P>::ES;
     const Rows a = {make_rsrc(I8 ? (const void*)p.xc : p.A, (int64_t)p.S * bytes),
                     lr < rows ? (shared ? f : f / p.k) * bytes : kPastEnd, bytes};
     asm volatile("" : "+v"(m.off));  // (addresses kept over the rounds spill)
-    Acc acc[Step<P>::NJ];
+    Acc acc[8];
     stream<P, SHARES, 3>(m, a, split * per + wave % SHARES, end, acc);
-    put_sums<P>(acc, red + wave * 16 * COLS, rows);
+    put_sums<P>(acc, red + wave * 16 * kCols, rows);
     __syncthreads();
     // the shares of K in their order, then the parts
-    Acc v[Q::N][2];
-    uint32_t o[Q::N];
+    Acc v[N][2];
+    uint32_t o[N];
 #pragma unroll
-    for (int i = 0; i < Q::N; ++i) {
-      const int r = r1 + i * Q::STRIDE;
+    for (int i = 0; i < N; ++i) {
+      const int r = r1 + i * STRIDE;
       o[i] = kPastEnd;
       v[i][0] = v[i][1] = Acc{};
       if (r >= rows) continue;
-      o[i] = (uint32_t)((base + w.rows[r0 + r]) * 2 * COLS + c) * 4;
+      if (d0 + c < D) o[i] = (uint32_t)(w.rows[r0 + r] * 2 * D + d0 + c) * 4;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const Val* q = red + (t * SHARES * 16 + r) * COLS + c;
+        const Val* q = red + (t * SHARES * 16 + r) * kCols + c;
         v[i][t] = *reinterpret_cast<const Acc*>(q) +
-                  *reinterpret_cast<const Acc*>(q + 16 * COLS);
+                  *reinterpret_cast<const Acc*>(q + 16 * kCols);
       }
     }
     if (p.splits > 1) {
 #pragma unroll
-      for (int i = 0; i < Q::N; ++i)
+      for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          store_shared(part, o[i] + split * one + t * COLS * 4,
+          store_shared(part, o[i] + split * one + t * D * 4,
                        __builtin_bit_cast(f32x4_t, v[i][t]));
       stores_done();
-      if (tid == 0) w.count[0] = count_up(p.split_done + at * p.rounds + r0 / 16);
+      if (tid == 0) w.count = count_up(p.split_done + at * p.rounds + r0 / 16);
       __syncthreads();
-      const bool last = uniform(w.count[0]) == p.splits - 1;
+      const bool last = uniform(w.count) == p.splits - 1;
       __syncthreads();
       if (!last) continue;
 #pragma unroll
-      for (int i = 0; i < Q::N; ++i) {
+      for (int i = 0; i < N; ++i) {
         Acc q[kMaxSplits][2];
 #pragma unroll
         for (int s = 0; s < kMaxSplits; ++s)
 #pragma unroll
           for (int t = 0; t < 2; ++t)
             q[s][t] = __builtin_bit_cast(
-                Acc, load_shared(part, s < p.splits ? o[i] + s * one + t * COLS * 4 : kPastEnd));
+                Acc, load_shared(part, s < p.splits ? o[i] + s * one + t * D * 4 : kPastEnd));
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           v[i][t] = q[0][t];
@@ -705,8 +723,8 @@ __global__ __launch_bounds__(kExpertThreads, 2) void few_up_kernel(FewArgs p) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < Q::N; ++i) {
-      const int r = r1 + i * Q::STRIDE;
+    for (int i = 0; i < N; ++i) {
+      const int r = r1 + i * STRIDE;
       if (r >= rows || d0 + c >= D) continue;
       const int row = w.rows[r0 + r];
       float u[4], g[4], hv[4];
@@ -731,9 +749,9 @@ __global__ __launch_bounds__(kExpertThreads, 2) void few_up_kernel(FewArgs p) {
     if constexpr (I8) {
       // the entry's last column group: codes of its rows
       stores_done();
-      if (tid == 0) w.count[0] = count_up(p.entry_done + (shared ? p.entries : 0) + entry);
+      if (tid == 0) w.count = count_up(p.entry_done + (shared ? p.entries : 0) + entry);
       __syncthreads();
-      const bool last = uniform(w.count[0]) == slices * ((n + 15) / 16) - 1;
+      const bool last = uniform(w.count) == slices * ((n + 15) / 16) - 1;
       __syncthreads();
       if (last)
         for (int r = wave; r < n; r += 4) {
@@ -742,57 +760,59 @@ __global__ __launch_bounds__(kExpertThreads, 2) void few_up_kernel(FewArgs p) {
                        p.hc + (shared ? (int64_t)p.F * p.D : 0) + (int64_t)row * D,
                        p.hs + base + row);
         }
-    } else if (r0 + 16 < n) {
+    } else if (r0 + 16 * blocks < n) {
       __syncthreads();
     }
   }
 }
 
-// Workgroup (entry, CT column tiles of H): waves CT x 4 / CT shares of D.
-template <int P, int CT>
-__global__ __launch_bounds__(kExpertThreads, 2) void few_down_kernel(FewArgs p) {
+// Workgroup (entry, CT column tiles of H): waves CT x SHARES of D.
+template <int P, int CT, int SHARES>
+__global__ __launch_bounds__(64 * CT * SHARES, 2) void few_down_kernel(FewArgs p) {
   using Val = typename Kind<P>::Val;
   using Acc = typename Kind<P>::Acc;
-  using Q = Quads<P>;
   constexpr bool I8 = P == kI8;
-  constexpr int COLS = Kind<P>::COLS, STEP = Kind<P>::STEP, SHARES = 4 / CT;
+  constexpr int PER_ROW = kCols / 4;
+  constexpr int STEP = Kind<P>::STEP, THREADS = 64 * CT * SHARES;
   constexpr int HS = P == kBf16 ? 2 : P == kF32 ? 4 : 1;  // bytes of the operand
-  __shared__ __align__(16) Val red[4 * 16 * COLS];
+  __shared__ __align__(16) Val red[CT * SHARES * 16 * kCols];
   __shared__ Work w;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
   const int all = uniform((int)blockIdx.x / p.cols), group = blockIdx.x - all * p.cols;
-  const bool shared = all >= p.entries;
-  const int entry = shared ? all - p.entries : all;
-  if (!find_work<kExpertThreads>(p, entry, shared, nullptr, w)) return;
+  const bool shared = all >= p.blocks * p.entries;
+  const int block = shared ? 0 : uniform(all / p.entries);
+  const int entry = all - (shared ? p.blocks : block) * p.entries;
+  const int blocks = shared ? 1 : p.blocks;
+  if (!find_work<THREADS>(p, entry, shared, nullptr, w)) return;
   const int n = uniform(w.n), e = shared ? 0 : uniform(w.expert);
   const int D = shared ? p.Ds : p.D, base = shared ? p.F : 0;
   const int64_t size = I8 ? i8_matrix_bytes(D, p.H) : (int64_t)D * p.H * Kind<P>::ES;
   const char* matrix = (shared ? p.ws[2] : p.w[2]) + e * size;
-  const int n0 = group * CT * COLS;
-  Columns<P> m(matrix, D, p.H, n0 + wave / SHARES * COLS);
+  const int n0 = group * CT * kCols;
+  Columns<P> m(matrix, D, p.H, n0 + wave / SHARES * kCols);
   const int steps = (D + STEP - 1) / STEP;
   const char* in = (I8 ? (const char*)p.hc : p.h) + (shared ? (int64_t)p.F * p.D * HS : 0);
   const uint32_t bytes = (uint32_t)D * HS;
   const rsrc_t y = make_rsrc(p.y, (int64_t)(p.F + p.S) * p.H * 4);
-  for (int r0 = 0; r0 < n; r0 += 16) {
+  for (int r0 = 16 * block; r0 < n; r0 += 16 * blocks) {
     const int rows = n - r0 < 16 ? n - r0 : 16;
     const int lr = lane & 15, f = lr < rows ? w.rows[r0 + lr] : 0;
     const Rows a = {make_rsrc(in, (int64_t)(shared ? p.S : p.F) * bytes),
                     lr < rows ? f * bytes : kPastEnd, bytes};
     asm volatile("" : "+v"(m.off));
-    Acc acc[Step<P>::NJ];
+    Acc acc[8];
     stream<P, SHARES, 3>(m, a, wave % SHARES, steps, acc);
-    put_sums<P>(acc, red + wave * 16 * COLS, rows);
+    put_sums<P>(acc, red + wave * 16 * kCols, rows);
     __syncthreads();
-    for (int i = tid; i < rows * CT * Q::PER_ROW; i += kExpertThreads) {
-      const int r = i / (CT * Q::PER_ROW), tile = i / Q::PER_ROW % CT, c = i % Q::PER_ROW * 4;
-      const int col = n0 + tile * COLS + c;
+    for (int i = tid; i < rows * CT * PER_ROW; i += THREADS) {
+      const int r = i / (CT * PER_ROW), tile = i / PER_ROW % CT, c = i % PER_ROW * 4;
+      const int col = n0 + tile * kCols + c;
       if (col >= p.H) continue;
-      const Val* q = red + (tile * SHARES * 16 + r) * COLS + c;
+      const Val* q = red + (tile * SHARES * 16 + r) * kCols + c;
       Acc v = *reinterpret_cast<const Acc*>(q);
 #pragma unroll
-      for (int s = 1; s < SHARES; ++s) v += *reinterpret_cast<const Acc*>(q + s * 16 * COLS);
+      for (int s = 1; s < SHARES; ++s) v += *reinterpret_cast<const Acc*>(q + s * 16 * kCols);
       const int row = base + w.rows[r0 + r];
       f32x4_t o;
       if constexpr (I8) {
@@ -806,10 +826,10 @@ __global__ __launch_bounds__(kExpertThreads, 2) void few_down_kernel(FewArgs p) 
       }
       store_shared(y, (uint32_t)(row * p.H + col) * 4, o);
     }
-    if (r0 + 16 < n) __syncthreads();
+    if (r0 + 16 * blocks < n) __syncthreads();
   }
   stores_done();
-  combine<kExpertThreads>(p, w, group, n0, CT * COLS);
+  combine<THREADS>(p, w, block, blocks, group, n0, CT * kCols);
 }
 
 // ------------------------------------------------------------ host
@@ -836,35 +856,35 @@ moe_status check_few(const moe_shape* s, bool i8) {
 
 struct FewWs {
   size_t words, score, xc, xs, h, hc, hs, part, y, total;
-  int entries, by_row, shared, slices, slices_s, splits, rounds, route_splits, tiles, cols;
+  int entries, by_row, shared, slices, slices_s, splits, rounds, blocks, route_splits,
+      tiles, shares, cols;
   int split_done, token_done, n_words;  // ints from words on
 };
 FewWs few_ws(const moe_shape* s, bool i8) {
   FewWs w = {};
   const int64_t F = s->S * s->k;
   auto up = [](int64_t a, int64_t b) { return (int)((a + b - 1) / b); };
-  const int cols = i8 ? kCols8 : kCols;
   w.by_row = F <= s->E;
   w.entries = (int)(w.by_row ? F : s->E);
   w.shared = s->D_shared ? up(s->S, 16) : 0;
-  w.slices = up(s->D, cols);
-  w.slices_s = s->D_shared ? up(s->D_shared, cols) : 0;
+  w.slices = up(s->D, kCols);
+  w.slices_s = s->D_shared ? up(s->D_shared, kCols) : 0;
   w.route_splits = up(s->H, kRouteRows);
-  // H in parts where there are not enough column groups for the CUs; few assignments, since
-  // each part keeps its sums of every one
+  // workgroups that share an expert's rounds of 16 rows where it has several as a rule
+  w.blocks = F > 8 * s->E ? (up(s->S, 16) < 8 ? up(s->S, 16) : 8) : 1;
+  // H in parts until there are kWanted workgroups (of entries that at least some have)
   const int groups = w.entries * w.slices + w.shared * w.slices_s;
-  w.splits = 1;
-  if (F <= kSplitRows && groups > 0) {
-    w.splits = kWanted / groups;
-    const int most = up(s->H, 2 * 64);  // two steps of bf16 for each wave
-    if (w.splits > most) w.splits = most;
-    if (w.splits > kMaxSplits) w.splits = kMaxSplits;
-    if (w.splits < 1) w.splits = 1;
-  }
+  int64_t splits = kWanted / ((int64_t)groups * w.blocks);
+  const int64_t most = up(s->H, 2 * 64);  // two steps of bf16 for each wave
+  if (splits > most) splits = most;
+  if (splits > kMaxSplits) splits = kMaxSplits;
+  w.splits = splits < 1 ? 1 : (int)splits;
   w.rounds = up(F > s->S ? F : s->S, 16);
   // two column tiles of H to a workgroup where that leaves enough of them
-  w.tiles = (w.entries + w.shared) * up(s->H, 2 * cols) >= 2 * kWanted ? 2 : 1;
-  w.cols = up(s->H, w.tiles * cols);
+  const int64_t all = (int64_t)w.blocks * w.entries + w.shared;
+  w.tiles = all * up(s->H, 2 * kCols) >= 1024 ? 2 : 1;
+  w.shares = all * up(s->H, kCols) <= 512 ? 8 : 4 / w.tiles;
+  w.cols = up(s->H, w.tiles * kCols);
   w.split_done = w.entries + w.shared;
   w.token_done = w.split_done + (w.splits > 1 ? groups * w.rounds : 0);
   w.n_words = w.token_done + (int)s->S * w.cols;
@@ -882,23 +902,30 @@ FewWs few_ws(const moe_shape* s, bool i8) {
   w.h = take(n_h * (!i8 && s->dtype == MOE_BF16 ? 2 : 4));
   w.hc = take(i8 ? n_h : 0);
   w.hs = take(i8 ? (size_t)(F + s->S) * 4 : 0);
-  w.part = take(w.splits > 1 ? (size_t)groups * w.splits * (F + s->S) * 2 * cols * 4 : 0);
+  w.part = take(w.splits > 1 ? n_h * w.splits * 2 * 4 : 0);
   w.y = take((size_t)(F + s->S) * s->H * 4);
   w.total = o ? o : 256;
   return w;
 }
 
+template <int P, int CT, int SHARES>
+void launch_down(const FewArgs& p, hipStream_t st) {
+  const unsigned grid = (unsigned)((p.blocks * p.entries + p.shared) * p.cols);
+  few_down_kernel<P, CT, SHARES><<<grid, 64 * CT * SHARES, 0, st>>>(p);
+}
+
 template <int P>
-void launch_experts(const FewArgs& p, int tiles, hipStream_t st) {
-  const unsigned groups = (unsigned)(p.entries * p.slices + p.shared * p.slices_s);
+void launch_experts(FewArgs p, const FewWs& z, hipStream_t st) {
+  const unsigned groups =
+      (unsigned)(p.blocks * p.entries * p.slices + p.shared * p.slices_s);
   few_up_kernel<P><<<groups * p.splits, kExpertThreads, 0, st>>>(p);
-  FewArgs d = p;
-  d.routed = 1;
-  const unsigned grid = (unsigned)((p.entries + p.shared) * p.cols);
-  if (tiles == 1)
-    few_down_kernel<P, 1><<<grid, kExpertThreads, 0, st>>>(d);
+  p.routed = 1;
+  if (z.tiles == 2)
+    launch_down<P, 2, 2>(p, st);
+  else if (z.shares == 8)
+    launch_down<P, 1, 8>(p, st);
   else
-    few_down_kernel<P, 2><<<grid, kExpertThreads, 0, st>>>(d);
+    launch_down<P, 1, 4>(p, st);
 }
 
 template <int R>
@@ -980,6 +1007,7 @@ moe_status few_forward(const moe_shape* s, bool i8, const void* A, const void* W
   p.slices_s = z.slices_s;
   p.splits = z.splits;
   p.rounds = z.rounds;
+  p.blocks = z.blocks;
   p.cols = z.cols;
   p.route_splits = z.route_splits;
   p.renormalize = s->renormalize;
@@ -994,11 +1022,11 @@ moe_status few_forward(const moe_shape* s, bool i8, const void* A, const void* W
     p.routed = 1;
   }
   if (i8)
-    launch_experts<kI8>(p, z.tiles, st);
+    launch_experts<kI8>(p, z, st);
   else if (s->dtype == MOE_F32)
-    launch_experts<kF32>(p, z.tiles, st);
+    launch_experts<kF32>(p, z, st);
   else
-    launch_experts<kBf16>(p, z.tiles, st);
+    launch_experts<kBf16>(p, z, st);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
