@@ -9,7 +9,8 @@
 //           completes
 // An entry is an expert with its rows, or the shared expert with 16 tokens. Up to 8 tokens
 // every workgroup of `up` sums the scores and selects the top-k for itself; beyond, a launch
-// of its own does it (one workgroup per token).
+// of its own does it (one workgroup per token), which also lists the experts' rows where
+// there are too many assignments for every workgroup to look through.
 //
 // Within a launch nothing waits: where there are few columns, H is cut in parts, and the last
 // of them to arrive adds the sums; the last of a token's entries to arrive at a column
@@ -52,6 +53,7 @@ constexpr int kMaxSplits = 8;        // parts of H
 constexpr int kWanted = 512;         // workgroups: as many as the chip holds
 constexpr int kRouteRows = 512;      // K rows of a router workgroup, 64 to a wave
 constexpr int kOwnRoute = 8;         // tokens that each workgroup routes for itself
+constexpr int kOwnList = kOwnRoute * 32;  // assignments up to which it looks for its own rows
 
 struct FewArgs {
   const void* A;
@@ -66,7 +68,9 @@ struct FewArgs {
   int* entry_done;     // [entries + shared] int8: arrived column groups of each 16 rows
   int* split_done;     // [column groups of D][rounds] arrived parts of H
   int* token_done;     // [S][column groups of H] arrived entries
+  int* expert_rows;    // [E] rows of each expert in `list` (more than kOwnList assignments)
   int n_words;         // of these
+  uint16_t* list;      // [E][F]
   int8_t* xc;          // int8: codes and scales of the tokens
   float* xs;
   char* h;             // [F][D], then [S][Ds] (fp32 with 8-bit weights)
@@ -407,15 +411,24 @@ __device__ __forceinline__ void sum_scores(const FewArgs& p, int t0, int tokens,
   }
 }
 
-// More than kOwnRoute tokens: a workgroup for each.
+// A workgroup for each token: more than kOwnRoute tokens are routed here; of more than kOwnList
+// assignments the experts' rows are listed, in the order in which they come (rows do not
+// meet in the products; every workgroup of the next launches sees the same list).
 __global__ __launch_bounds__(256) void few_topk_kernel(FewArgs p) {
   __shared__ float g[1024];
-  const int t = blockIdx.x;
-  sum_scores(p, t, 1, threadIdx.x, 256, g);
-  __syncthreads();
-  if (threadIdx.x < 64)
-    topk_one(g, p.E, p.k, p.renormalize, p.ids + (int64_t)t * p.k, p.tw + (int64_t)t * p.k,
-             threadIdx.x);
+  const int t = blockIdx.x, lane = threadIdx.x;
+  int32_t* ids = p.ids + (int64_t)t * p.k;
+  if (p.Wr != nullptr) {
+    sum_scores(p, t, 1, threadIdx.x, 256, g);
+    __syncthreads();
+    if (lane < 64)
+      topk_one(g, p.E, p.k, p.renormalize, ids, p.tw + (int64_t)t * p.k, lane);
+  }
+  if (p.F > kOwnList && lane < p.k) {
+    const int id = ids[lane];  // this thread's own store, or given
+    if (id >= 0 && id < p.E)
+      p.list[(int64_t)id * p.F + count_up(p.expert_rows + id)] = (uint16_t)(t * p.k + lane);
+  }
 }
 
 // ------------------------------------------------------------ experts
@@ -425,19 +438,20 @@ struct Work {
   int n;           // rows
   int expert;      // -1: shared
   int count;
-  int part[8], first[8];
+  int part[8];
   int done[64];    // tokens complete
   uint16_t rows[kMaxRows];       // assignments (shared: tokens)
-  int ids[kOwnRoute * 32];       // of the tokens that this workgroup has routed for itself
-  float tw[kOwnRoute * 32];
+  int ids[kOwnList];       // of the tokens that this workgroup has routed for itself
+  float tw[kOwnList];
 };
 
-// Routes where that is this workgroup's to do, and finds entry y's expert and rows; false:
-// nothing to do. lds: kOwnRoute x 1024 floats.
+// Routes where that is this workgroup's to do, and finds entry y's expert e; false: there is
+// none, or it is an earlier entry's. lds: kOwnRoute x 1024 floats.
 template <int THREADS>
-__device__ __forceinline__ bool find_work(const FewArgs& p, int y, bool shared, float* lds,
-                                          Work& w) {
+__device__ __forceinline__ bool find_expert(const FewArgs& p, int y, bool shared, float* lds,
+                                            Work& w, int& e) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  static_assert(THREADS >= kOwnList, "a thread for each assignment");
   if (!p.routed) {
     sum_scores(p, 0, p.S, tid, THREADS, lds);
     __syncthreads();
@@ -451,68 +465,58 @@ __device__ __forceinline__ bool find_work(const FewArgs& p, int y, bool shared, 
     if (blockIdx.x == 0)  // the weights are the next launch's
       for (int t = wave; t < p.S; t += THREADS / 64)
         topk_one(lds + t * p.E, p.E, p.k, p.renormalize, p.ids + t * p.k, p.tw + t * p.k, lane);
-  } else if (p.F <= kOwnRoute * 32) {
-    for (int f = tid; f < p.F; f += THREADS) {
-      w.ids[f] = p.ids[f];
-      w.tw[f] = p.tw[f];
+  } else if (p.F <= kOwnList) {
+    if (tid < p.F) {
+      w.ids[tid] = p.ids[tid];
+      w.tw[tid] = p.tw[tid];
     }
     __syncthreads();
   }
-  if (shared) {
-    const int n = p.S - 16 * y < 16 ? p.S - 16 * y : 16;
-    if (tid < n) w.rows[tid] = (uint16_t)(16 * y + tid);
-    if (tid == 0) {
-      w.n = n;
-      w.expert = -1;
-    }
-    __syncthreads();
-    return true;
-  }
-  const bool here = p.F <= kOwnRoute * 32;
-  const int e = uniform(!p.by_row ? y : here ? w.ids[y] : p.ids[y]);
+  e = 0;
+  if (shared) return true;
+  e = y;
+  if (!p.by_row) return true;
+  e = uniform(w.ids[y]);
   if (e < 0 || e >= p.E) return false;
-  // each wave a stretch of the assignments, in their order: workgroups that share the rows
-  // list them alike
-  const int per = (p.F + THREADS - 1) / THREADS * 64, f0 = wave * per;
-  const int f1 = f0 + per < p.F ? f0 + per : p.F;
-  auto mine = [&](int f) { return f < f1 && (here ? w.ids[f] : p.ids[f]) == e; };
-  int n = 0, first = p.F;
-  for (int f = f0; f < f1; f += 64) {
-    const uint64_t b = __ballot(mine(f + lane));
-    if (n == 0 && b != 0) first = f + (int)__builtin_ctzll(b);
-    n += (int)__popcll(b);
-  }
-  if (lane == 0) {
-    w.part[wave] = n;
-    w.first[wave] = first;
-  }
-  __syncthreads();
-  int at = 0, all = 0;
-  first = p.F;
+  return !__syncthreads_or(tid < y && w.ids[tid] == e);
+}
+
+// Its rows; false: there are none.
+template <int THREADS>
+__device__ __forceinline__ bool find_rows(const FewArgs& p, int y, bool shared, int e, Work& w) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  int n;
+  if (shared) {
+    n = p.S - 16 * y < 16 ? p.S - 16 * y : 16;
+    if (tid < n) w.rows[tid] = (uint16_t)(16 * y + tid);
+  } else if (p.F <= kOwnList) {
+    const bool mine = tid < p.F && w.ids[tid] == e;
+    const uint64_t b = __ballot(mine);
+    if (lane == 0) w.part[wave] = (int)__popcll(b);
+    __syncthreads();
+    int at = 0;
+    n = 0;
 #pragma unroll
-  for (int i = 0; i < THREADS / 64; ++i) {
-    if (i < wave) at += w.part[i];
-    all += w.part[i];
-    first = first < w.first[i] ? first : w.first[i];
-  }
-  if (uniform(all) == 0 || (p.by_row && uniform(first) != y)) return false;  // an earlier entry's
-  if (n > 0)
-    for (int f = f0; f < f1; f += 64) {
-      const bool m = mine(f + lane);
-      const uint64_t b = __ballot(m);
-      if (m) w.rows[at + __popcll(b & ((1ull << lane) - 1))] = (uint16_t)(f + lane);
-      at += (int)__popcll(b);
+    for (int i = 0; i < THREADS / 64; ++i) {
+      if (i < wave) at += w.part[i];
+      n += w.part[i];
     }
+    if (mine) w.rows[at + __popcll(b & ((1ull << lane) - 1))] = (uint16_t)tid;
+  } else {
+    n = p.expert_rows[e];
+    for (int i = tid; i < n; i += THREADS) w.rows[i] = p.list[(int64_t)e * p.F + i];
+  }
+  n = uniform(n);
   if (tid == 0) {
-    w.n = all;
-    w.expert = e;
+    w.n = n;
+    w.expert = shared ? -1 : e;
   }
   __syncthreads();
-  return true;
+  return n > 0;
 }
 
 __device__ __forceinline__ bool valid_slot(const FewArgs& p, const Work& w, int f) {
-  const int id = p.F <= kOwnRoute * 32 ? w.ids[f] : p.ids[f];
+  const int id = p.F <= kOwnList ? w.ids[f] : p.ids[f];
   return id >= 0 && id < p.E;
 }
 
@@ -558,7 +562,7 @@ __device__ __forceinline__ void combine(const FewArgs& p, Work& w, int block, in
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int f = t * p.k + (j0 + j < p.k ? j0 + j : 0);
-          const float wt = p.F <= kOwnRoute * 32 ? w.tw[f] : p.tw[f];
+          const float wt = p.F <= kOwnList ? w.tw[f] : p.tw[f];
           const bool in = j0 + j < p.k && valid_slot(p, w, f);
 #pragma unroll
           for (int q = 0; q < 4; ++q) a[q] = in ? a[q] + wt * v[j][q] : a[q];
@@ -580,28 +584,34 @@ __device__ __forceinline__ void combine(const FewArgs& p, Work& w, int block, in
 }
 
 // This wave's share of K's steps below `end`: every SHARES-th from `first` on.
-template <int P, int SHARES, int DEPTH>
-__device__ __forceinline__ void stream(const Columns<P>& m, const Rows& a, int first, int end,
-                                       typename Kind<P>::Acc (&acc)[8]) {
+template <int P, int SHARES>
+struct Stream {
+  static constexpr int DEPTH = 3;
   Step<P> st[DEPTH];
   uint4 x[DEPTH];
+
+  // the first loads of weights, which may go out before the rows are known
+  __device__ __forceinline__ void start(const Columns<P>& m, int first, int end) {
 #pragma unroll
-  for (int d = 0; d < DEPTH; ++d) {
-    st[d].load(m, first + d * SHARES, end);
-    x[d] = a.load(first + d * SHARES, end);
+    for (int d = 0; d < DEPTH; ++d) st[d].load(m, first + d * SHARES, end);
   }
+  __device__ __forceinline__ void run(const Columns<P>& m, const Rows& a, int first, int end,
+                                      typename Kind<P>::Acc (&acc)[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = typename Kind<P>::Acc{};
-  for (int s = first; s < end;) {
+    for (int d = 0; d < DEPTH; ++d) x[d] = a.load(first + d * SHARES, end);
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d, s += SHARES) {
-      st[d].compute(x[d], acc);
-      st[d].load(m, s + DEPTH * SHARES, end);
-      x[d] = a.load(s + DEPTH * SHARES, end);
-      __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not behind the next step
+    for (int j = 0; j < 8; ++j) acc[j] = typename Kind<P>::Acc{};
+    for (int s = first; s < end;) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d, s += SHARES) {
+        st[d].compute(x[d], acc);
+        st[d].load(m, s + DEPTH * SHARES, end);
+        x[d] = a.load(s + DEPTH * SHARES, end);
+        __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not behind the next step
+      }
     }
   }
-}
+};
 
 // Row f's codes and scale from its fp32 values, by one wave (twice read).
 __device__ __forceinline__ void quantize_row(rsrc_t h, uint32_t row, int D, int8_t* codes,
@@ -647,14 +657,19 @@ __global__ __launch_bounds__(kExpertThreads, 2) void few_up_kernel(FewArgs p) {
   const int e0 = uniform(g0 / slices), d0 = (g0 - e0 * slices) * kCols;
   const int block = shared ? 0 : uniform(e0 / p.entries), entry = e0 - block * p.entries;
   const int blocks = shared ? 1 : p.blocks;
-  if (!find_work<kExpertThreads>(p, entry, shared, reinterpret_cast<float*>(red), w)) return;
-  const int n = uniform(w.n), e = shared ? 0 : uniform(w.expert);
+  int e;
+  if (!find_expert<kExpertThreads>(p, entry, shared, reinterpret_cast<float*>(red), w, e)) return;
   const int D = shared ? p.Ds : p.D;
   const int64_t size = I8 ? i8_matrix_bytes(p.H, D) : (int64_t)p.H * D * Kind<P>::ES;
   const char* const* mats = shared ? p.ws : p.w;
   const int steps = (p.H + STEP - 1) / STEP, per = uniform((steps + p.splits - 1) / p.splits);
   const int end = (split + 1) * per < steps ? (split + 1) * per : steps;
   Columns<P> m(mats[wave / SHARES] + e * size, p.H, D, d0);
+  const int first = split * per + wave % SHARES;
+  Stream<P, SHARES> sm;
+  sm.start(m, first, end);
+  if (!find_rows<kExpertThreads>(p, entry, shared, e, w)) return;
+  const int n = uniform(w.n);
   const int base = shared ? p.F : 0;
   const int at = shared ? p.entries * p.slices + g0 : g0 - block * p.entries * p.slices;
   const rsrc_t h = make_rsrc(p.h + (shared ? (int64_t)p.F * p.D * HS : 0),
@@ -672,7 +687,8 @@ __global__ __launch_bounds__(kExpertThreads, 2) void few_up_kernel(FewArgs p) {
                     lr < rows ? (shared ? f : f / p.k) * bytes : kPastEnd, bytes};
     asm volatile("" : "+v"(m.off));  // (addresses kept over the rounds spill)
     Acc acc[8];
-    stream<P, SHARES, 3>(m, a, split * per + wave % SHARES, end, acc);
+    if (r0 > 16 * block) sm.start(m, first, end);
+    sm.run(m, a, first, end, acc);
     put_sums<P>(acc, red + wave * 16 * kCols, rows);
     __syncthreads();
     // the shares of K in their order, then the parts
@@ -784,14 +800,18 @@ __global__ __launch_bounds__(64 * CT * SHARES, 2) void few_down_kernel(FewArgs p
   const int block = shared ? 0 : uniform(all / p.entries);
   const int entry = all - (shared ? p.blocks : block) * p.entries;
   const int blocks = shared ? 1 : p.blocks;
-  if (!find_work<THREADS>(p, entry, shared, nullptr, w)) return;
-  const int n = uniform(w.n), e = shared ? 0 : uniform(w.expert);
+  int e;
+  if (!find_expert<THREADS>(p, entry, shared, nullptr, w, e)) return;
   const int D = shared ? p.Ds : p.D, base = shared ? p.F : 0;
   const int64_t size = I8 ? i8_matrix_bytes(D, p.H) : (int64_t)D * p.H * Kind<P>::ES;
   const char* matrix = (shared ? p.ws[2] : p.w[2]) + e * size;
   const int n0 = group * CT * kCols;
   Columns<P> m(matrix, D, p.H, n0 + wave / SHARES * kCols);
   const int steps = (D + STEP - 1) / STEP;
+  Stream<P, SHARES> sm;
+  sm.start(m, wave % SHARES, steps);
+  if (!find_rows<THREADS>(p, entry, shared, e, w)) return;
+  const int n = uniform(w.n);
   const char* in = (I8 ? (const char*)p.hc : p.h) + (shared ? (int64_t)p.F * p.D * HS : 0);
   const uint32_t bytes = (uint32_t)D * HS;
   const rsrc_t y = make_rsrc(p.y, (int64_t)(p.F + p.S) * p.H * 4);
@@ -802,7 +822,8 @@ __global__ __launch_bounds__(64 * CT * SHARES, 2) void few_down_kernel(FewArgs p
                     lr < rows ? f * bytes : kPastEnd, bytes};
     asm volatile("" : "+v"(m.off));
     Acc acc[8];
-    stream<P, SHARES, 3>(m, a, wave % SHARES, steps, acc);
+    if (r0 > 16 * block) sm.start(m, wave % SHARES, steps);
+    sm.run(m, a, wave % SHARES, steps, acc);
     put_sums<P>(acc, red + wave * 16 * kCols, rows);
     __syncthreads();
     for (int i = tid; i < rows * CT * PER_ROW; i += THREADS) {
@@ -855,16 +876,16 @@ moe_status check_few(const moe_shape* s, bool i8) {
 }
 
 struct FewWs {
-  size_t words, score, xc, xs, h, hc, hs, part, y, total;
+  size_t words, list, score, xc, xs, h, hc, hs, part, y, total;
   int entries, by_row, shared, slices, slices_s, splits, rounds, blocks, route_splits,
       tiles, shares, cols;
-  int split_done, token_done, n_words;  // ints from words on
+  int split_done, token_done, expert_rows, n_words;  // ints from words on
 };
 FewWs few_ws(const moe_shape* s, bool i8) {
   FewWs w = {};
   const int64_t F = s->S * s->k;
   auto up = [](int64_t a, int64_t b) { return (int)((a + b - 1) / b); };
-  w.by_row = F <= s->E;
+  w.by_row = F <= s->E && F <= kOwnList;
   w.entries = (int)(w.by_row ? F : s->E);
   w.shared = s->D_shared ? up(s->S, 16) : 0;
   w.slices = up(s->D, kCols);
@@ -887,7 +908,8 @@ FewWs few_ws(const moe_shape* s, bool i8) {
   w.cols = up(s->H, w.tiles * kCols);
   w.split_done = w.entries + w.shared;
   w.token_done = w.split_done + (w.splits > 1 ? groups * w.rounds : 0);
-  w.n_words = w.token_done + (int)s->S * w.cols;
+  w.expert_rows = w.token_done + (int)s->S * w.cols;
+  w.n_words = w.expert_rows + (F > kOwnList ? (int)s->E : 0);
   size_t o = 0;
   auto take = [&](size_t n) {
     const size_t at = o;
@@ -896,6 +918,7 @@ FewWs few_ws(const moe_shape* s, bool i8) {
   };
   const size_t n_h = (size_t)(F * s->D + s->S * s->D_shared);
   w.words = take((size_t)w.n_words * 4);
+  w.list = take(F > kOwnList ? (size_t)(s->E * F) * 2 : 0);
   w.score = take((size_t)w.route_splits * s->S * s->E * 4);
   w.xc = take(i8 ? (size_t)s->S * s->H : 0);
   w.xs = take(i8 ? (size_t)s->S * 4 : 0);
@@ -985,7 +1008,9 @@ moe_status few_forward(const moe_shape* s, bool i8, const void* A, const void* W
   p.entry_done = (int*)(ws + z.words);
   p.split_done = p.entry_done + z.split_done;
   p.token_done = p.entry_done + z.token_done;
+  p.expert_rows = p.entry_done + z.expert_rows;
   p.n_words = z.n_words;
+  p.list = (uint16_t*)(ws + z.list);
   p.xc = (int8_t*)(ws + z.xc);
   p.xs = (float*)(ws + z.xs);
   p.h = ws + z.h;
@@ -1016,11 +1041,9 @@ moe_status few_forward(const moe_shape* s, bool i8, const void* A, const void* W
     launch_route<kF32>(p, i8, st);
   else
     launch_route<kBf16>(p, i8, st);
-  p.routed = W_router == nullptr;
-  if (W_router != nullptr && p.S > kOwnRoute) {
+  p.routed = W_router == nullptr || p.S > kOwnRoute;
+  if ((W_router != nullptr && p.S > kOwnRoute) || p.F > kOwnList)
     few_topk_kernel<<<(unsigned)p.S, 256, 0, st>>>(p);
-    p.routed = 1;
-  }
   if (i8)
     launch_experts<kI8>(p, z, st);
   else if (s->dtype == MOE_F32)
