@@ -445,13 +445,14 @@ struct Work {
   float tw[kOwnList];
 };
 
-// Routes where that is this workgroup's to do, and finds entry y's expert e; false: there is
-// none, or it is an earlier entry's. lds: kOwnRoute x 1024 floats.
+// Entry y's expert e (routed first where that is this workgroup's to do); false: there is none.
+// lds: kOwnRoute x 1024 floats.
 template <int THREADS>
 __device__ __forceinline__ bool find_expert(const FewArgs& p, int y, bool shared, float* lds,
                                             Work& w, int& e) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  static_assert(THREADS >= kOwnList, "a thread for each assignment");
+  e = 0;
+  if (shared) return true;
   if (!p.routed) {
     sum_scores(p, 0, p.S, tid, THREADS, lds);
     __syncthreads();
@@ -465,31 +466,29 @@ __device__ __forceinline__ bool find_expert(const FewArgs& p, int y, bool shared
     if (blockIdx.x == 0)  // the weights are the next launch's
       for (int t = wave; t < p.S; t += THREADS / 64)
         topk_one(lds + t * p.E, p.E, p.k, p.renormalize, p.ids + t * p.k, p.tw + t * p.k, lane);
-  } else if (p.F <= kOwnList) {
+  }
+  e = p.by_row ? uniform(p.routed ? p.ids[y] : w.ids[y]) : y;
+  return e >= 0 && e < p.E;
+}
+
+// Its rows; false: there are none, or they are an earlier entry's.
+template <int THREADS>
+__device__ __forceinline__ bool find_rows(const FewArgs& p, int y, bool shared, int e, Work& w) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  static_assert(THREADS >= kOwnList, "a thread for each assignment");
+  const bool own = p.F <= kOwnList;
+  if (own && p.routed) {
     if (tid < p.F) {
       w.ids[tid] = p.ids[tid];
       w.tw[tid] = p.tw[tid];
     }
     __syncthreads();
   }
-  e = 0;
-  if (shared) return true;
-  e = y;
-  if (!p.by_row) return true;
-  e = uniform(w.ids[y]);
-  if (e < 0 || e >= p.E) return false;
-  return !__syncthreads_or(tid < y && w.ids[tid] == e);
-}
-
-// Its rows; false: there are none.
-template <int THREADS>
-__device__ __forceinline__ bool find_rows(const FewArgs& p, int y, bool shared, int e, Work& w) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   int n;
   if (shared) {
     n = p.S - 16 * y < 16 ? p.S - 16 * y : 16;
     if (tid < n) w.rows[tid] = (uint16_t)(16 * y + tid);
-  } else if (p.F <= kOwnList) {
+  } else if (own) {
     const bool mine = tid < p.F && w.ids[tid] == e;
     const uint64_t b = __ballot(mine);
     if (lane == 0) w.part[wave] = (int)__popcll(b);
@@ -512,7 +511,7 @@ __device__ __forceinline__ bool find_rows(const FewArgs& p, int y, bool shared, 
     w.expert = shared ? -1 : e;
   }
   __syncthreads();
-  return n > 0;
+  return n > 0 && (shared || !p.by_row || uniform(w.rows[0]) == y);
 }
 
 __device__ __forceinline__ bool valid_slot(const FewArgs& p, const Work& w, int f) {
