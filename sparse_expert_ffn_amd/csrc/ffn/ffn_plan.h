@@ -111,11 +111,12 @@ inline void apply_plan(const GemmPlan& p, GemmArgs* g, void* part) {
   g->part = (float*)part;
 }
 
+// join: false where the caller adds the splits' sums itself.
 template <typename Core, typename EP>
-void launch_tile(const GemmArgs& g, const EP& ep, hipStream_t st) {
+void launch_tile(const GemmArgs& g, const EP& ep, hipStream_t st, bool join = true) {
   const unsigned grid = (unsigned)((int64_t)g.tiles_m * g.tiles_n * g.splits);
   gemm_kernel<Core, EP><<<grid, Core::THREADS, 0, st>>>(g, ep);
-  if (g.splits > 1) {
+  if (g.splits > 1 && join) {
     const int64_t n = g.M * ((g.N + 3) / 4);
     const int64_t b = (n + 255) / 256;
     gemm_join_kernel<Core::DUAL, typename Core::Val, EP><<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(g, ep);

@@ -6,6 +6,7 @@
 // Weights are packed once in the MFMA's operand order.
 #include "ffn_plan.h"
 #include "i8.h"
+#include "stream.h"
 
 namespace moe {
 namespace {
@@ -23,12 +24,31 @@ struct Chunk<bf16_t> {
   Pack<bf16_t, 8> v[2];
   __device__ __forceinline__ void load(const bf16_t* p) { v[0].load(p), v[1].load(p + 8); }
   __device__ __forceinline__ float get(int i) const { return v[i / 8].get(i % 8); }
+  // abs_bits of the largest magnitude; magnitudes as 16-bit integers, two at a time
+  __device__ __forceinline__ uint32_t top() const {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      m = __builtin_elementwise_max(
+          m, __builtin_bit_cast(u16x2_t, v[i / 4].w[i % 4] & 0x7FFF7FFFu));
+    return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+  }
 };
 template <>
 struct Chunk<float> {
   Pack<float, 16> v;
   __device__ __forceinline__ void load(const float* p) { v.load(p); }
   __device__ __forceinline__ float get(int i) const { return v.get(i); }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t b = abs_bits(v.get(i));
+      m = m > b ? m : b;
+    }
+    return m;
+  }
 };
 
 // TPR threads to a row, NC chunks of 16 values each in registers; of a longer row the
@@ -50,20 +70,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void quantize_rows_kernel(
     if (lane + n * TPR < chunks) c[n].load(x + (int64_t)(lane + n * TPR) * 16);
 #pragma unroll
   for (int n = 0; n < NC; ++n)
-    if (lane + n * TPR < chunks)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t b = abs_bits(c[n].get(i));
-        top = top > b ? top : b;
-      }
+    if (lane + n * TPR < chunks) {
+      const uint32_t b = c[n].top();
+      top = top > b ? top : b;
+    }
   for (int at = lane + NC * TPR; at < chunks; at += TPR) {
     Chunk<T> w;
     w.load(x + (int64_t)at * 16);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t b = abs_bits(w.get(i));
-      top = top > b ? top : b;
-    }
+    const uint32_t b = w.top();
+    top = top > b ? top : b;
   }
   top = wave_max_u32(top);
   if constexpr (TPR > 64) {
@@ -75,12 +90,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void quantize_rows_kernel(
   const Quant q(top);
   if (lane == 0) scales[row] = q.scale;
   auto put = [&](int at, const Chunk<T>& w) {
-    uint32_t d[4];
+    float v[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      d[i] = q.pack4(w.get(4 * i), w.get(4 * i + 1), w.get(4 * i + 2), w.get(4 * i + 3));
-    *reinterpret_cast<uint4*>(codes + row * K + (int64_t)at * 16) =
-        make_uint4(d[0], d[1], d[2], d[3]);
+    for (int i = 0; i < 16; ++i) v[i] = w.get(i);
+    *reinterpret_cast<uint4*>(codes + row * K + (int64_t)at * 16) = q.pack16(v);
   };
 #pragma unroll
   for (int n = 0; n < NC; ++n)
@@ -253,41 +266,232 @@ struct EpI8Swiglu {
   __device__ __forceinline__ void operator()(int64_t m, int64_t n, const int (&a)[W],
                                              const int (&b)[W], const Pre<W>& p) const {
     float v[W];
+    values(a, b, p, v);
+    store_n(h + m * ld + n, v);
+  }
+  template <int W>
+  __device__ __forceinline__ static void values(const int (&a)[W], const int (&b)[W],
+                                                const Pre<W>& p, float (&v)[W]) {
 #pragma unroll
     for (int r = 0; r < W; ++r)
       v[r] = silu_f32((float)a[r] * p.x * p.u[r]) * ((float)b[r] * p.x * p.g[r]);
-    store_n(h + m * ld + n, v);
   }
 };
 
+// Where K was split: a workgroup adds a row's sums, forms h and quantises it at once (as a join
+// and the rows' quantisation of their own 8.7 us at 64 x 2048). D up to kJoinCols.
+constexpr int kJoinCols = 8192;
+__global__ __launch_bounds__(512) void i8_join_kernel(GemmArgs g, EpI8Swiglu ep, int8_t* codes,
+                                                      float* scales) {
+  constexpr int NC = kJoinCols / 4 / 512;
+  __shared__ uint32_t tops[8];
+  const int64_t m = blockIdx.x, panel = g.M * g.N;
+  const int* part = reinterpret_cast<const int*>(g.part) + m * g.N;
+  float h[NC][4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int n = (i * 512 + (int)threadIdx.x) * 4;
+    if (n >= g.N) continue;
+    EpI8Swiglu::Pre<4> pre;
+    ep.pre(m, n, pre);
+    int v[2][4] = {};
+    for (int s = 0; s < g.splits; s += 4) {
+      i32x4_t w[4][2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          w[e][p] = s + e < g.splits ? *reinterpret_cast<const i32x4_t*>(
+                                           part + ((s + e) * 2 + p) * panel + n)
+                                     : i32x4_t{};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[p][r] += w[e][p][r];
+    }
+    ep.values(v[0], v[1], pre, h[i]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t b = abs_bits(h[i][r]);
+      top = top > b ? top : b;
+    }
+  }
+  top = wave_max_u32(top);
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x / 64] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) top = top > tops[w] ? top : tops[w];
+  const Quant q(top);
+  if (threadIdx.x == 0) scales[m] = q.scale;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int n = (i * 512 + (int)threadIdx.x) * 4;
+    if (n < g.N)
+      *reinterpret_cast<uint32_t*>(codes + m * g.N + n) =
+          q.pack4(h[i][0], h[i][1], h[i][2], h[i][3]);
+  }
+}
+
 template <bool DUAL, typename EP>
-void launch_i8(const GemmPlan& p, const GemmArgs& g, const EP& ep, hipStream_t st) {
+void launch_i8(const GemmPlan& p, const GemmArgs& g, const EP& ep, hipStream_t st,
+               bool join) {
   constexpr int NP = DUAL ? 2 : 1;
   using T = int8_t;
   if (p.tile == 0)
-    launch_tile<TileCore<T, 256, 256, 2, DUAL, true, true, 2, 4, 2>>(g, ep, st);
+    launch_tile<TileCore<T, 256, 256, 2, DUAL, true, true, 2, 4, 2>>(g, ep, st, join);
   else if (p.tile == 1)
-    launch_tile<TileCore<T, 128, 128, NP, DUAL, true, true, 2, 4, 2>>(g, ep, st);
+    launch_tile<TileCore<T, 128, 128, NP, DUAL, true, true, 2, 4, 2>>(g, ep, st, join);
   else if (p.tile == 4)
-    launch_tile<TileCore<T, 256, 128, NP, DUAL, true, true, 4, 2, 3>>(g, ep, st);
+    launch_tile<TileCore<T, 256, 128, NP, DUAL, true, true, 4, 2, 3>>(g, ep, st, join);
   else if (p.tile == 2 && p.tiles_m == 1)
-    launch_tile<TileCore<T, 64, 128, NP, DUAL, true, true, 2, 4, 3, true>>(g, ep, st);
+    launch_tile<TileCore<T, 64, 128, NP, DUAL, true, true, 2, 4, 3, true>>(g, ep, st, join);
   else if (p.tile == 2)
-    launch_tile<TileCore<T, 64, 128, NP, DUAL, true, true, 2, 4, 3>>(g, ep, st);
+    launch_tile<TileCore<T, 64, 128, NP, DUAL, true, true, 2, 4, 3>>(g, ep, st, join);
   else if (p.tiles_m == 1)
-    launch_tile<TileCore<T, 16, 128, NP, DUAL, true, true, 1, 4, 4, true>>(g, ep, st);
+    launch_tile<TileCore<T, 16, 128, NP, DUAL, true, true, 1, 4, 4, true>>(g, ep, st, join);
   else
-    launch_tile<TileCore<T, 16, 128, NP, DUAL, true, true, 1, 4, 4>>(g, ep, st);
+    launch_tile<TileCore<T, 16, 128, NP, DUAL, true, true, 1, 4, 4>>(g, ep, st, join);
+}
+
+// Up to 16 rows in one launch, quantisation included: a workgroup of 16 waves takes 16 columns,
+// a sixteenth of K to each wave. The weight's first loads go out before the rows are read;
+// every workgroup quantises the rows for itself into LDS. One row of 7168 x 2048: 8.2 us
+// in a row, 6.2 of them the kernel's (quantised by a launch of its own and split over K with
+// an arrival count, 14).
+constexpr int kFewThreads = 1024, kFewWaves = kFewThreads / 64;
+constexpr int kFewRows = 16;
+constexpr int64_t kFewCodes = 128 * 1024;  // bytes of LDS for the rows' codes
+struct FewRows {
+  const void* X;
+  const float* sx;  // given: X holds codes
+  const char* W;
+  void* Y;
+  int S, K, N;
+  int per_row;      // waves that quantise a row
+};
+
+template <typename T, typename OUT>
+__global__ __launch_bounds__(kFewThreads) void i8_few_kernel(FewRows p) {
+  constexpr int DEPTH = 8;
+  extern __shared__ __align__(16) char codes[];  // [S][K + 16]
+  __shared__ __align__(16) int red[kFewWaves * 16 * 16];
+  __shared__ uint32_t tops[kFewWaves];
+  __shared__ float scales[kFewRows];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int kt = (int)i8_tiles_k(p.K), pitch = p.K + 16, n0 = blockIdx.x * kI8TileN;
+  const rsrc_t w = make_rsrc(p.W + (int64_t)blockIdx.x * kt * 1024, (int64_t)kt * 1024);
+  auto load = [&](int s) {  // past the last tile: zeros
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                         w, s < kt ? (uint32_t)s * 1024 + lane * 16 : kPastEnd, 0,
+                                         kNonTemporal));
+  };
+  uint4 st[DEPTH];
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) st[d] = load(wave + d * kFewWaves);
+  const int chunks = p.K / 16;
+  if (p.sx != nullptr) {
+    const char* x = (const char*)p.X;
+    for (int i = tid; i < p.S * chunks; i += kFewThreads) {
+      const int r = i / chunks, c = i - r * chunks;
+      *reinterpret_cast<uint4*>(codes + r * pitch + c * 16) =
+          *reinterpret_cast<const uint4*>(x + (int64_t)i * 16);
+    }
+    if (tid < p.S) scales[tid] = p.sx[tid];
+  } else {
+    const int row = wave / p.per_row, c0 = wave % p.per_row * 64 + lane;
+    const T* x = (const T*)p.X + (int64_t)row * p.K;
+    uint32_t top = 0;
+    if (row < p.S)
+      for (int c = c0; c < chunks; c += p.per_row * 64) {
+        Chunk<T> v;
+        v.load(x + c * 16);
+        const uint32_t b = v.top();
+        top = top > b ? top : b;
+      }
+    top = wave_max_u32(top);
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    if (row < p.S) {
+      for (int i = 0; i < p.per_row; ++i) {
+        const uint32_t b = tops[row * p.per_row + i];
+        top = top > b ? top : b;
+      }
+      const Quant q(top);
+      if (c0 == 0) scales[row] = q.scale;
+      for (int c = c0; c < chunks; c += p.per_row * 64) {  // from the caches
+        Chunk<T> v;
+        v.load(x + c * 16);
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = v.get(i);
+        *reinterpret_cast<uint4*>(codes + row * pitch + c * 16) = q.pack16(f);
+      }
+    }
+  }
+  __syncthreads();
+  // rows that are not there take row 0's codes: their sums are not read. K values behind the
+  // end meet weights of zero
+  const int lr = lane & 15, g = lane >> 4;
+  const char* xr = codes + (lr < p.S ? lr : 0) * pitch + g * 16;
+  i32x4_t acc = {0, 0, 0, 0};
+  for (int s = wave; s < kt;) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d, s += kFewWaves) {
+      if (s < kt) {
+        const int at = s * 64 + g * 16 < p.K ? s * 64 : 0;
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+            *reinterpret_cast<const i32x4_t*>(xr + at), __builtin_bit_cast(i32x4_t, st[d]), acc,
+            0, 0, 0);
+      }
+      st[d] = load(s + DEPTH * kFewWaves);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) red[(wave * 16 + 4 * g + r) * 16 + lr] = acc[r];
+  __syncthreads();
+  const int r = tid / 16, n = n0 + tid % 16;
+  if (r >= p.S || n >= p.N) return;
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < kFewWaves; ++i) sum += red[i * 256 + tid];
+  const float* sw = reinterpret_cast<const float*>(p.W + i8_code_bytes(p.K, p.N));
+  const float y = (float)sum * scales[r] * sw[n];
+  reinterpret_cast<OUT*>(p.Y)[(int64_t)r * p.N + n] = from_f32<OUT>(y);
+}
+
+// Against the tiles with the rows' quantisation before them: 1 x 7168 x 2048 8.2 and 15.2 us, 16
+// rows 12.6 and 15.6, 13 x 2064 x 5128 13.2 and 14.8; but 16 x 8192 x 8192 21.3 and 20.7, 1 x
+// 768 x 16384 14.5 and 11.3 (more workgroups than the chip holds twice, each of which
+// quantises the rows).
+bool few_rows(int64_t S, int64_t K, int64_t N) {
+  return S <= kFewRows && S * (K + 16) <= kFewCodes && i8_tiles_n(N) <= 400;
+}
+
+template <typename T, typename OUT>
+hipError_t launch_few_rows(const FewRows& p, hipStream_t st) {
+  const size_t lds = (size_t)p.S * (p.K + 16);
+  if (lds > 48 * 1024) {
+    const hipError_t e =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(i8_few_kernel<T, OUT>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)kFewCodes);
+    if (e != hipSuccess) return e;
+  }
+  i8_few_kernel<T, OUT><<<(unsigned)i8_tiles_n(p.N), kFewThreads, lds, st>>>(p);
+  return hipGetLastError();
 }
 
 const float* scales_of(const void* W, int64_t K, int64_t N) {
   return reinterpret_cast<const float*>((const char*)W + i8_code_bytes(K, N));
 }
 
-// A product of rows of codes with one packed matrix, or two (DUAL).
+// A product of rows of codes with one packed matrix, or two (DUAL); returns its arguments.
 template <bool DUAL, typename EP>
-void run_i8(const GemmPlan& p, int64_t M, int64_t K, int64_t N, const int8_t* X, const void* W0,
-            const void* W1, const EP& ep, void* part, hipStream_t st) {
+GemmArgs run_i8(const GemmPlan& p, int64_t M, int64_t K, int64_t N, const int8_t* X,
+                const void* W0, const void* W1, const EP& ep, void* part, hipStream_t st,
+                bool join = true) {
   GemmArgs g = {};
   g.A[0] = X;
   g.B[0][0] = W0;
@@ -299,7 +503,8 @@ void run_i8(const GemmPlan& p, int64_t M, int64_t K, int64_t N, const int8_t* X,
   g.K[0] = K;
   g.pairs = 1;
   apply_plan(p, &g, part);
-  launch_i8<DUAL>(p, g, ep, st);
+  launch_i8<DUAL>(p, g, ep, st, join);
+  return g;
 }
 
 GemmPlan plan_i8(bool dual, int64_t M, int64_t N, int64_t K) {
@@ -308,16 +513,18 @@ GemmPlan plan_i8(bool dual, int64_t M, int64_t N, int64_t K) {
 
 struct MatmulWs {
   GemmPlan p;
+  bool few;
   size_t codes, scales, part, total;
 };
 MatmulWs matmul_ws(int64_t S, int64_t K, int64_t N) {
-  MatmulWs w;
+  MatmulWs w = {};
+  w.few = few_rows(S, K, N);
+  w.total = 256;
+  if (w.few) return w;
   w.p = plan_i8(false, S, N, K);
-  w.codes = 0;
   w.scales = ffn_round_up((size_t)S * K, 256);
   w.part = w.scales + ffn_round_up((size_t)S * 4, 256);
   w.total = w.part + ffn_round_up(w.p.part_bytes, 256);
-  if (w.total == 0) w.total = 256;
   return w;
 }
 
@@ -326,7 +533,7 @@ struct FfnWs {
   size_t xc, xs, h, hc, hs, part, total;
 };
 FfnWs ffn_ws(const moe_ffn_shape* s) {
-  FfnWs w;
+  FfnWs w = {};
   w.up = plan_i8(true, s->S, s->D, s->H);
   w.down = plan_i8(false, s->S, s->H, s->D);
   size_t o = 0;
@@ -443,8 +650,8 @@ extern "C" moe_status moe_quantize_i8_rows(const void* X, int64_t S, int64_t K, 
   if (X == nullptr || codes == nullptr || scales == nullptr || ffn_shared({codes, scales}, {X}))
     return MOE_ERR_INVALID_ARGUMENT;
   if (!ffn_aligned16(X) || !ffn_aligned16(codes) || !aligned4(scales)) return MOE_ERR_UNSUPPORTED;
-  return launch_quantize_rows(X, S, K, dtype == MOE_F32, codes, scales, (hipStream_t)stream) ==
-                 hipSuccess
+  return launch_quantize_rows(X, S, K, dtype == MOE_F32, codes, scales,
+                              (hipStream_t)stream) == hipSuccess
              ? MOE_OK
              : MOE_ERR_HIP;
 }
@@ -476,15 +683,25 @@ extern "C" moe_status moe_i8_matmul(int64_t S, int64_t K, int64_t N, int32_t dty
   hipStream_t sq = (hipStream_t)stream;
   char* ws = (char*)workspace;
   const int8_t* codes = (const int8_t*)X;
+  const bool f32 = dtype == MOE_F32, out_f32 = f32 || (flags & MOE_OUTPUT_F32) != 0;
+  if (w.few) {
+    int per = kFewWaves;
+    while (per * S > kFewWaves) per /= 2;
+    const FewRows a = {X, row_scales, (const char*)W, Y, (int)S, (int)K, (int)N, per};
+    const hipError_t e = f32       ? launch_few_rows<float, float>(a, sq)
+                         : out_f32 ? launch_few_rows<bf16_t, float>(a, sq)
+                                   : launch_few_rows<bf16_t, bf16_t>(a, sq);
+    return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  }
   if (row_scales == nullptr) {
     codes = (int8_t*)(ws + w.codes);
     row_scales = (float*)(ws + w.scales);
-    if (launch_quantize_rows(X, S, K, dtype == MOE_F32, (int8_t*)(ws + w.codes),
-                             (float*)(ws + w.scales), sq) != hipSuccess)
+    if (launch_quantize_rows(X, S, K, f32, (int8_t*)(ws + w.codes), (float*)(ws + w.scales),
+                             sq) != hipSuccess)
       return MOE_ERR_HIP;
   }
   const float* sw = scales_of(W, K, N);
-  if (dtype == MOE_F32 || (flags & MOE_OUTPUT_F32))
+  if (out_f32)
     run_i8<false>(w.p, S, K, N, codes, W, nullptr,
                   EpI8Store<float>{(float*)Y, row_scales, sw, N}, ws + w.part, sq);
   else
@@ -516,11 +733,15 @@ extern "C" moe_status moe_i8_ffn_forward(const moe_ffn_shape* s, const void* X, 
   float *xs = (float*)(ws + w.xs), *hs = (float*)(ws + w.hs), *h = (float*)(ws + w.h);
   const bool f32 = s->dtype == MOE_F32;
   if (launch_quantize_rows(X, s->S, s->H, f32, xc, xs, sq) != hipSuccess) return MOE_ERR_HIP;
-  run_i8<true>(w.up, s->S, s->H, s->D, xc, W_up, W_gate,
-               EpI8Swiglu{h, xs, scales_of(W_up, s->H, s->D), scales_of(W_gate, s->H, s->D),
-                          s->D},
-               ws + w.part, sq);
-  if (launch_quantize_rows(h, s->S, s->D, true, hc, hs, sq) != hipSuccess) return MOE_ERR_HIP;
+  const EpI8Swiglu swiglu = {h, xs, scales_of(W_up, s->H, s->D), scales_of(W_gate, s->H, s->D),
+                             s->D};
+  const bool join_here = w.up.splits > 1 && s->D <= kJoinCols;
+  const GemmArgs g = run_i8<true>(w.up, s->S, s->H, s->D, xc, W_up, W_gate, swiglu, ws + w.part,
+                                  sq, !join_here);
+  if (join_here)
+    i8_join_kernel<<<(unsigned)s->S, 512, 0, sq>>>(g, swiglu, hc, hs);
+  else if (launch_quantize_rows(h, s->S, s->D, true, hc, hs, sq) != hipSuccess)
+    return MOE_ERR_HIP;
   const float* sd = scales_of(W_down, s->D, s->H);
   if (f32 || (s->flags & MOE_OUTPUT_F32))
     run_i8<false>(w.down, s->S, s->D, s->H, hc, W_down, nullptr,
