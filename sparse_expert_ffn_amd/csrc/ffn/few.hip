@@ -523,15 +523,19 @@ __global__ __launch_bounds__(kExpertThreads, 2) void few_up_kernel(FewArgs p) {
       if (r >= rows || d0 + c >= D) continue;
       const int row = w.rows[r0 + r];
       float u[4], g[4], hv[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) u[q] = (float)v[i][0][q], g[q] = (float)v[i][1][q];
       if constexpr (I8) {
         const float x = p.xs[shared ? row : row / p.k];
         const int64_t sc = e * size + i8_code_bytes(p.H, D);
         const f32x4_t su = load4(reinterpret_cast<const float*>(mats[0] + sc) + d0 + c);
         const f32x4_t sg = load4(reinterpret_cast<const float*>(mats[1] + sc) + d0 + c);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) u[q] = u[q] * x * su[q], g[q] = g[q] * x * sg[q];
+        for (int q = 0; q < 4; ++q) {
+          u[q] = scaled(v[i][0][q], x, su[q]);
+          g[q] = scaled(v[i][1][q], x, sg[q]);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u[q] = v[i][0][q], g[q] = v[i][1][q];
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) hv[q] = silu_f32(u[q]) * g[q];
@@ -620,7 +624,7 @@ __global__ __launch_bounds__(64 * CT * SHARES, 2) void few_down_kernel(FewArgs p
         const f32x4_t sw =
             load4(reinterpret_cast<const float*>(matrix + i8_code_bytes(D, p.H)) + col);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = (float)v[q] * hs * sw[q];
+        for (int q = 0; q < 4; ++q) o[q] = scaled(v[q], hs, sw[q]);
       } else {
         o = v;
       }

@@ -238,7 +238,7 @@ struct EpI8Store {
                                              const int (&)[W], const Pre<W>& p) const {
     float v[W];
 #pragma unroll
-    for (int r = 0; r < W; ++r) v[r] = (float)a[r] * p.x * p.w[r];
+    for (int r = 0; r < W; ++r) v[r] = scaled(a[r], p.x, p.w[r]);
     store_n(out + m * ld + n, v);
   }
 };
@@ -274,7 +274,7 @@ struct EpI8Swiglu {
                                                 const Pre<W>& p, float (&v)[W]) {
 #pragma unroll
     for (int r = 0; r < W; ++r)
-      v[r] = silu_f32((float)a[r] * p.x * p.u[r]) * ((float)b[r] * p.x * p.g[r]);
+      v[r] = silu_f32(scaled(a[r], p.x, p.u[r])) * scaled(b[r], p.x, p.g[r]);
   }
 };
 
@@ -356,12 +356,12 @@ void launch_i8(const GemmPlan& p, const GemmArgs& g, const EP& ep, hipStream_t s
     launch_tile<TileCore<T, 16, 128, NP, DUAL, true, true, 1, 4, 4>>(g, ep, st, join);
 }
 
-// Up to 16 rows in one launch, quantisation included: a workgroup of 16 waves takes 16 columns,
-// a sixteenth of K to each wave. The weight's first loads go out before the rows are read;
-// every workgroup quantises the rows for itself into LDS. One row of 7168 x 2048: 8.2 us
-// in a row, 6.2 of them the kernel's (quantised by a launch of its own and split over K with
-// an arrival count, 14).
-constexpr int kFewThreads = 1024, kFewWaves = kFewThreads / 64;
+// Up to 16 rows in one launch, quantisation included: a workgroup of 8 waves takes 16 columns,
+// an eighth of K to each wave. The weight's first loads go out before the rows are read;
+// every workgroup quantises the rows for itself into LDS. One row of 7168 x 2048 8.4 us in a
+// row, 6.2 of them the kernel's: its latency (quantised by a launch of its own and split over
+// K with an arrival count, 14). 16 waves are as fast with one workgroup to a CU (8.3), slower
+// with more (13 x 2064 x 5128: 9.7 and 12.7 us).
 constexpr int kFewRows = 16;
 constexpr int64_t kFewCodes = 128 * 1024;  // bytes of LDS for the rows' codes
 struct FewRows {
@@ -373,12 +373,14 @@ struct FewRows {
   int per_row;      // waves that quantise a row
 };
 
+constexpr int kFewWaves = 8;
 template <typename T, typename OUT>
-__global__ __launch_bounds__(kFewThreads) void i8_few_kernel(FewRows p) {
-  constexpr int DEPTH = 8;
+__global__ __launch_bounds__(64 * kFewWaves) void i8_few_kernel(FewRows p) {
+  constexpr int DEPTH = 8, WAVES = kFewWaves, THREADS = 64 * WAVES;
+  constexpr int NC = 4;  // chunks of a row that a thread keeps between its two passes
   extern __shared__ __align__(16) char codes[];  // [S][K + 16]
-  __shared__ __align__(16) int red[kFewWaves * 16 * 16];
-  __shared__ uint32_t tops[kFewWaves];
+  __shared__ __align__(16) int red[WAVES * 16 * 16];
+  __shared__ uint32_t tops[WAVES];
   __shared__ float scales[kFewRows];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int kt = (int)i8_tiles_k(p.K), pitch = p.K + 16, n0 = blockIdx.x * kI8TileN;
@@ -390,45 +392,68 @@ __global__ __launch_bounds__(kFewThreads) void i8_few_kernel(FewRows p) {
   };
   uint4 st[DEPTH];
 #pragma unroll
-  for (int d = 0; d < DEPTH; ++d) st[d] = load(wave + d * kFewWaves);
+  for (int d = 0; d < DEPTH; ++d) st[d] = load(wave + d * WAVES);
   const int chunks = p.K / 16;
   if (p.sx != nullptr) {
     const char* x = (const char*)p.X;
-    for (int i = tid; i < p.S * chunks; i += kFewThreads) {
+    for (int i = tid; i < p.S * chunks; i += THREADS) {
       const int r = i / chunks, c = i - r * chunks;
       *reinterpret_cast<uint4*>(codes + r * pitch + c * 16) =
           *reinterpret_cast<const uint4*>(x + (int64_t)i * 16);
     }
     if (tid < p.S) scales[tid] = p.sx[tid];
   } else {
-    const int row = wave / p.per_row, c0 = wave % p.per_row * 64 + lane;
-    const T* x = (const T*)p.X + (int64_t)row * p.K;
-    uint32_t top = 0;
-    if (row < p.S)
-      for (int c = c0; c < chunks; c += p.per_row * 64) {
-        Chunk<T> v;
-        v.load(x + c * 16);
-        const uint32_t b = v.top();
-        top = top > b ? top : b;
-      }
-    top = wave_max_u32(top);
-    if (lane == 0) tops[wave] = top;
-    __syncthreads();
-    if (row < p.S) {
-      for (int i = 0; i < p.per_row; ++i) {
-        const uint32_t b = tops[row * p.per_row + i];
-        top = top > b ? top : b;
+    const int stride = p.per_row * 64, c0 = wave % p.per_row * 64 + lane;
+    for (int r0 = 0; r0 < p.S; r0 += WAVES / p.per_row) {
+      const int row = r0 + wave / p.per_row;
+      const bool in = row < p.S;
+      const T* x = (const T*)p.X + (int64_t)row * p.K;
+      Chunk<T> keep[NC];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (in && c0 + i * stride < chunks) keep[i].load(x + (c0 + i * stride) * 16);
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (in && c0 + i * stride < chunks) {
+          const uint32_t b = keep[i].top();
+          top = top > b ? top : b;
+        }
+      if (in)
+        for (int c = c0 + NC * stride; c < chunks; c += stride) {
+          Chunk<T> v;
+          v.load(x + c * 16);
+          const uint32_t b = v.top();
+          top = top > b ? top : b;
+        }
+      top = wave_max_u32(top);
+      if (p.per_row > 1) {
+        if (lane == 0) tops[wave] = top;
+        __syncthreads();
+        for (int i = 0; i < p.per_row; ++i) {
+          const uint32_t b = tops[wave / p.per_row * p.per_row + i];
+          top = top > b ? top : b;
+        }
       }
       const Quant q(top);
-      if (c0 == 0) scales[row] = q.scale;
-      for (int c = c0; c < chunks; c += p.per_row * 64) {  // from the caches
-        Chunk<T> v;
-        v.load(x + c * 16);
+      auto put = [&](const Chunk<T>& v, int c) {
         float f[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) f[i] = v.get(i);
         *reinterpret_cast<uint4*>(codes + row * pitch + c * 16) = q.pack16(f);
+      };
+      if (in) {
+        if (c0 == 0) scales[row] = q.scale;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          if (c0 + i * stride < chunks) put(keep[i], c0 + i * stride);
+        for (int c = c0 + NC * stride; c < chunks; c += stride) {  // from the caches
+          Chunk<T> v;
+          v.load(x + c * 16);
+          put(v, c);
+        }
       }
+      if (p.per_row > 1) __syncthreads();
     }
   }
   __syncthreads();
@@ -439,39 +464,40 @@ __global__ __launch_bounds__(kFewThreads) void i8_few_kernel(FewRows p) {
   i32x4_t acc = {0, 0, 0, 0};
   for (int s = wave; s < kt;) {
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d, s += kFewWaves) {
+    for (int d = 0; d < DEPTH; ++d, s += WAVES) {
       if (s < kt) {
         const int at = s * 64 + g * 16 < p.K ? s * 64 : 0;
         acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
             *reinterpret_cast<const i32x4_t*>(xr + at), __builtin_bit_cast(i32x4_t, st[d]), acc,
             0, 0, 0);
       }
-      st[d] = load(s + DEPTH * kFewWaves);
+      st[d] = load(s + DEPTH * WAVES);
     }
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) red[(wave * 16 + 4 * g + r) * 16 + lr] = acc[r];
   __syncthreads();
   const int r = tid / 16, n = n0 + tid % 16;
-  if (r >= p.S || n >= p.N) return;
+  if (tid >= 256 || r >= p.S || n >= p.N) return;
   int sum = 0;
 #pragma unroll
-  for (int i = 0; i < kFewWaves; ++i) sum += red[i * 256 + tid];
+  for (int i = 0; i < WAVES; ++i) sum += red[i * 256 + tid];
   const float* sw = reinterpret_cast<const float*>(p.W + i8_code_bytes(p.K, p.N));
-  const float y = (float)sum * scales[r] * sw[n];
+  const float y = scaled(sum, scales[r], sw[n]);
   reinterpret_cast<OUT*>(p.Y)[(int64_t)r * p.N + n] = from_f32<OUT>(y);
 }
 
-// Against the tiles with the rows' quantisation before them: 1 x 7168 x 2048 8.2 and 15.2 us, 16
-// rows 12.6 and 15.6, 13 x 2064 x 5128 13.2 and 14.8; but 16 x 8192 x 8192 21.3 and 20.7, 1 x
-// 768 x 16384 14.5 and 11.3 (more workgroups than the chip holds twice, each of which
-// quantises the rows).
+// Against the tiles with the rows' quantisation before them: 1 x 7168 x 2048 8.4 and 16.4 us, 16
+// rows 13.7 and 16.7; 1 x 768 x 16384 9.6 and 12.3; 16 x 8192 x 8192 21.5 and 21.7; but 16 x
+// 768 x 16384 13.5 and 12.4: each workgroup quantises all rows.
 bool few_rows(int64_t S, int64_t K, int64_t N) {
-  return S <= kFewRows && S * (K + 16) <= kFewCodes && i8_tiles_n(N) <= 400;
+  return S <= kFewRows && S * (K + 16) <= kFewCodes && S * i8_tiles_n(N) <= 8192;
 }
 
 template <typename T, typename OUT>
-hipError_t launch_few_rows(const FewRows& p, hipStream_t st) {
+hipError_t launch_few_rows(FewRows p, hipStream_t st) {
+  p.per_row = kFewWaves;
+  while (p.per_row > 1 && p.per_row * p.S > kFewWaves) p.per_row /= 2;
   const size_t lds = (size_t)p.S * (p.K + 16);
   if (lds > 48 * 1024) {
     const hipError_t e =
@@ -479,10 +505,9 @@ hipError_t launch_few_rows(const FewRows& p, hipStream_t st) {
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)kFewCodes);
     if (e != hipSuccess) return e;
   }
-  i8_few_kernel<T, OUT><<<(unsigned)i8_tiles_n(p.N), kFewThreads, lds, st>>>(p);
+  i8_few_kernel<T, OUT><<<(unsigned)i8_tiles_n(p.N), 64 * kFewWaves, lds, st>>>(p);
   return hipGetLastError();
 }
-
 const float* scales_of(const void* W, int64_t K, int64_t N) {
   return reinterpret_cast<const float*>((const char*)W + i8_code_bytes(K, N));
 }
@@ -568,9 +593,9 @@ moe_status check_rows(int64_t S, int64_t N) {
   return MOE_OK;
 }
 
-// A launch of a workgroup of up to 1024 threads per row.
+// A launch of up to 1024 threads per row, below 2^32 in all.
 bool rows_fit(int64_t S, int64_t K) {
-  return K <= 64 * 64 ? S < (int64_t)1 << 26 : K <= 256 * 64 ? S < 1 << 24 : S < 1 << 22;
+  return K <= 64 * 64 ? S < (1 << 26) - 4 : K <= 256 * 64 ? S < 1 << 24 : S < 1 << 22;
 }
 
 moe_status check_i8_ffn(const moe_ffn_shape* s) {
@@ -685,9 +710,7 @@ extern "C" moe_status moe_i8_matmul(int64_t S, int64_t K, int64_t N, int32_t dty
   const int8_t* codes = (const int8_t*)X;
   const bool f32 = dtype == MOE_F32, out_f32 = f32 || (flags & MOE_OUTPUT_F32) != 0;
   if (w.few) {
-    int per = kFewWaves;
-    while (per * S > kFewWaves) per /= 2;
-    const FewRows a = {X, row_scales, (const char*)W, Y, (int)S, (int)K, (int)N, per};
+    const FewRows a = {X, row_scales, (const char*)W, Y, (int)S, (int)K, (int)N, 0};
     const hipError_t e = f32       ? launch_few_rows<float, float>(a, sq)
                          : out_f32 ? launch_few_rows<bf16_t, float>(a, sq)
                                    : launch_few_rows<bf16_t, bf16_t>(a, sq);
