@@ -212,7 +212,8 @@ moe_status moe_quantize_i8_rows(const void* X, int64_t S, int64_t K, int32_t dty
 
 /*
  * Y = X W in that arithmetic: Y_sn = (sum_k xcode_sk wcode_kn) xscale_s wscale_n, the
- * sum exact in integers, scaled in fp32, rounded once. Any S: one token to a prompt.
+ * sum exact in integers, scaled in fp32 (the smaller scale first), rounded once. Any S:
+ * one token to a prompt; a row's result does not depend on S.
  *   row_scales  NULL: X is [S][K] of `dtype` (MOE_F32 or MOE_BF16), quantised by the
  *               call as moe_quantize_i8_rows does.
  *               [S] fp32: X holds [S][K] codes (int8) with these scales
@@ -239,8 +240,9 @@ moe_status moe_i8_ffn_forward(const moe_ffn_shape* shape, const void* X, const v
                               size_t workspace_bytes, void* stream);
 
 /*
- * The whole MoE layer for a few tokens (decode), in three launches: gate scores, softmax
- * top-k, the experts, the shared expert and the combine.
+ * The whole MoE layer for a few tokens (decode): gate scores, softmax top-k, the
+ * experts, the shared expert and the combine, in three launches (four beyond 8 tokens or
+ * 256 assignments).
  *   G = A W_router (+ router_bias); topk_ids, topk_weights from G as moe_gate_topk's
  *   O_t = sum_j topk_weights[t][j] FFN_{topk_ids[t][j]}(A_t)  (+ FFN_shared(A_t))
  * in slot order, then the shared expert. An expert's weights are read once per 16 of
@@ -254,16 +256,12 @@ moe_status moe_i8_ffn_forward(const moe_ffn_shape* shape, const void* X, const v
  *                then router_bias) inputs: the routing is given, an id outside [0, E) is
  *                a slot without an expert (it contributes nothing, whatever its weight)
  *   O            [S][H] dtype, or fp32 with MOE_OUTPUT_F32
- * Scores are summed in fp32 over up to 256 values of H, these sums in double, and
+ * Scores are summed in fp32 over up to 512 values of H, these sums in double, and
  * rounded to fp32; a NaN score ranks as -inf. Sums of the products are fp32, in an order
- * that depends on the shape and on how many experts the tokens have chosen (so the same
- * call gives the same bits); in bf16 mode h is rounded once to bf16.
- * H, D, D_shared multiples of 8 up to 65536, one matrix below 0x7F000000 bytes (with 64
- * rows and columns more), 16-byte aligned arrays (else MOE_ERR_UNSUPPORTED).
- *
- * The second launch's workgroups wait for each other's results. A wait never depends on a
- * workgroup that has not started; should one last some seconds all the same (a GPU that
- * is taken away meanwhile), the call gives up and the rows of O that are missing are NaN.
+ * that the shape alone fixes; in bf16 mode h is rounded once to bf16. Workgroups count each
+ * other's arrivals and never wait for one another.
+ * H, D, D_shared multiples of 8 up to 65536, one matrix (with 64 rows and columns more)
+ * below 0x7F000000 bytes, 16-byte aligned arrays (else MOE_ERR_UNSUPPORTED).
  *
  * moe_few_i8_forward takes expert weights packed by moe_pack_i8_weights (E matrices; the
  * shared expert's with E = 1) and computes each expert as moe_i8_ffn_forward does; dtype

@@ -327,7 +327,7 @@ class I8FFNBuffers:
 
 
 class FewMoEBuffers:
-    """The whole MoE layer for up to 128 tokens in two launches. i8: expert weights in 8
+    """The whole MoE layer for up to 128 tokens in few launches. i8: expert weights in 8
     bits (I8Weight; dtype MOE_BF16)."""
 
     def __init__(self, S, H, D, E, k, D_shared=0, renormalize=1, dtype=MOE_BF16, i8=False,
