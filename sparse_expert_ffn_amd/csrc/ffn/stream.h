@@ -87,7 +87,7 @@ struct Kind<kI8> {
   static constexpr int ES = 1, STEP = 64;
 };
 
-// A wave's columns of a matrix [K][N] from n0 on, K values from k0 on.
+// A wave's columns of a matrix [K][N] from n0 on.
 template <int P>
 struct Columns {
   rsrc_t r;
@@ -95,18 +95,18 @@ struct Columns {
   uint32_t past[P == kF32 ? 2 : 1];  // fp32: two halves of 64 columns, which end at N each
 
   __device__ __forceinline__ Columns() {}
-  __device__ __forceinline__ Columns(const char* matrix, int K, int N, int n0, int k0 = 0) {
+  __device__ __forceinline__ Columns(const char* matrix, int K, int N, int n0) {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     if constexpr (P == kI8) {
       const uint32_t kt = (uint32_t)i8_tiles_k(K);
       r = make_rsrc(matrix, n0 < N ? i8_code_bytes(K, N) : 0);
-      off = (uint32_t)((n0 / 16) * kt + k0 / 64) * 1024 + lane * 16;
+      off = (uint32_t)((n0 / 16) * kt) * 1024 + lane * 16;
       row = kt * 1024;
       step = 1024;
     } else {
       constexpr int ES = Kind<P>::ES;
       r = make_rsrc(matrix, (int64_t)K * N * ES);
-      off = (uint32_t)((k0 + (P == kBf16 ? 8 : 4) * g) * N + n0 + (P == kBf16 ? 8 : 4) * c) * ES;
+      off = (uint32_t)((P == kBf16 ? 8 : 4) * g * N + n0 + (P == kBf16 ? 8 : 4) * c) * ES;
       if constexpr (P == kBf16) {
         if (n0 + 8 * c >= N) off = kPastEnd;
       } else {

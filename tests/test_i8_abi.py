@@ -76,7 +76,8 @@ def test_matmul(lib):
     assert f(Y=A[0]) == INVALID and f(Y=A[1]) == INVALID and f(rs=A[2]) == INVALID
     assert f(ws=A[0]) == INVALID and f(ws=A[2]) == INVALID and f(ws=A[5] + 4) == UNSUPPORTED
     need = moe.moe_i8_matmul_workspace_bytes(4, 64, 16)
-    assert need >= 4 * 64 + 16
+    assert need > 0  # few rows are quantised in the product's launch, more before it
+    assert moe.moe_i8_matmul_workspace_bytes(4000, 64, 16) >= 4000 * (64 + 4)
     assert f(n=need - 1) == SMALL and f(ws=None) == SMALL
     assert f(S=0, X=None, Y=None) == OK
 
