@@ -514,8 +514,8 @@ struct TileCore {
   }
 
   // Consecutive columns of one row that a lane handles in the epilogue: the MFMA
-  // leaves 4; but in fp32 two neighbouring blocks swap lane rows to make it 8, one
-  // 16-byte access.
+  // leaves 4; with operands of 2 bytes or 1 two neighbouring blocks swap lane rows to
+  // make it 8, one 16-byte access.
   static constexpr int W = sizeof(T) <= 2 && NIP % 2 == 0 ? 8 : 4;
   static constexpr int BPG = W / 4;            // blocks per group of W columns
   static constexpr int GROUPS = (DUAL ? NIP : NI) / BPG;  // per row block

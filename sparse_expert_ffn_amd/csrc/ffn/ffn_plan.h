@@ -124,7 +124,8 @@ void launch_tile(const GemmArgs& g, const EP& ep, hipStream_t st, bool join = tr
   if (g.splits > 1 && join) {
     const int64_t n = g.M * ((g.N + 3) / 4);
     const int64_t b = (n + 255) / 256;
-    gemm_join_kernel<Core::DUAL, typename Core::Val, EP><<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(g, ep);
+    gemm_join_kernel<Core::DUAL, typename Core::Val, EP>
+        <<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(g, ep);
   }
 }
 

@@ -508,6 +508,7 @@ hipError_t launch_few_rows(FewRows p, hipStream_t st) {
   i8_few_kernel<T, OUT><<<(unsigned)i8_tiles_n(p.N), 64 * kFewWaves, lds, st>>>(p);
   return hipGetLastError();
 }
+
 const float* scales_of(const void* W, int64_t K, int64_t N) {
   return reinterpret_cast<const float*>((const char*)W + i8_code_bytes(K, N));
 }

@@ -182,6 +182,7 @@ struct Rows {
     return load16(r, s < end && at < bytes ? off + at : kPastEnd);
   }
 };
+
 // This lane's sums into LDS as rows of the wave's columns: rows 4 (l / 16) .. + 3 below n.
 template <int P>
 __device__ __forceinline__ void put_sums(const typename Kind<P>::Acc (&acc)[8],
