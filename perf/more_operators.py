@@ -120,11 +120,18 @@ def _normal(gen, shape, std, dtype):
     return (torch.randn(shape, generator=gen, device=DEV) * std).to(dtype)
 
 
-def _quant(x, dim):
-    """Codes (int8) and scales of a float tensor, one scale per vector along dim."""
-    s = x.float().abs().amax(dim, keepdim=True) / 127.0
+def _codes(x, s):
+    """Codes (int8) of a float tensor with scales s."""
     q = torch.round(x.double() / s.double())
-    return torch.where(s > 0, q, 0.0).clamp(-127, 127).to(torch.int8), s
+    return torch.where(s > 0, q, 0.0).clamp(-127, 127).to(torch.int8)
+
+
+def _quant(x, dim):
+    """Codes and scales of a float tensor, one scale per vector along dim. The quotient in 64
+    bits, rounded once: a device tensor over a number is a product with the number's
+    reciprocal, in 32 bits an ulp off in 3 to 6% of the vectors."""
+    s = (x.abs().amax(dim, keepdim=True).double() / 127).float()
+    return _codes(x, s), s
 
 
 def _w8(gen, E, K, N):
@@ -132,8 +139,9 @@ def _w8(gen, E, K, N):
     q = torch.empty((E, K, N), dtype=torch.int8, device=DEV)
     s = torch.empty((E, N), device=DEV)
     for e in range(E):
-        q[e], se = _quant(_normal(gen, (K, N), 1 / math.sqrt(K), torch.bfloat16), 0)
-        s[e] = se[0]
+        w = _normal(gen, (K, N), 1 / math.sqrt(K), torch.bfloat16)
+        s[e] = w.float().abs().amax(0) / 127.0  # an input: whatever scales the user has
+        q[e] = _codes(w, s[e])
     return q, s
 
 
