@@ -666,6 +666,8 @@ struct FewWs {
 };
 FewWs few_ws(const moe_shape* s, bool i8) {
   FewWs w = {};
+  w.total = 256;
+  if (s->S == 0) return w;  // no entries to divide workgroups among
   const int64_t F = s->S * s->k;
   auto up = [](int64_t a, int64_t b) { return (int)((a + b - 1) / b); };
   w.by_row = F <= s->E && F <= kOwnList;
@@ -710,7 +712,7 @@ FewWs few_ws(const moe_shape* s, bool i8) {
   w.hs = take(i8 ? (size_t)(F + s->S) * 4 : 0);
   w.part = take(w.splits > 1 ? n_h * w.splits * 2 * 4 : 0);
   w.y = take((size_t)(F + s->S) * s->H * 4);
-  w.total = o ? o : 256;
+  w.total = o;
   return w;
 }
 
