@@ -190,7 +190,7 @@ moe_status moe_w4_forward(const moe_shape* shape, int32_t group, const void* A,
  *
  * moe_quantize_i8 gives the codes [E][K][N] and scales [E][N] of a bf16 or fp32
  * tensor W [E][K][N]. moe_pack_i8_weights lays codes and scales, of whatever
- * quantiser (codes of -128 are allowed), out for the products below:
+ * quantiser (codes of -128 and scales below 0 are allowed), out for the products below:
  * moe_i8_weight_bytes(E, K, N) bytes at `packed`. Layout, matrix by matrix: tiles of
  * 16 columns n by 64 rows k, column tile by column tile, k ascending, 1024 bytes each:
  * 16 bytes for each lane l = 16 q + c, rows 16 q .. + 15 of column c; then the scales,
@@ -212,7 +212,7 @@ moe_status moe_quantize_i8_rows(const void* X, int64_t S, int64_t K, int32_t dty
 
 /*
  * Y = X W in that arithmetic: Y_sn = (sum_k xcode_sk wcode_kn) xscale_s wscale_n, the
- * sum exact in integers, scaled in fp32 (the smaller scale first), rounded once. Any S:
+ * sum exact in integers, scaled in fp32 (the scale nearer to 0 first), rounded once. Any S:
  * one token to a prompt; a row's result does not depend on S.
  *   row_scales  NULL: X is [S][K] of `dtype` (MOE_F32 or MOE_BF16), quantised by the
  *               call as moe_quantize_i8_rows does.

@@ -29,11 +29,11 @@ __host__ __device__ inline int64_t i8_matrix_bytes(int64_t K, int64_t N) {
 // maximum of them loses neither.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// A sum of products of codes times both scales. The smaller scale first: the sum is a whole
+// A sum of products of codes times both scales. The one nearer to 0 first: the sum is a whole
 // number, so nothing between overflows or leaves the normal range that the result does not.
 // (A scale of NaN stays.)
 __device__ __forceinline__ float scaled(int sum, float a, float b) {
-  const bool a_is_more = a > b;
+  const bool a_is_more = __builtin_fabsf(a) > __builtin_fabsf(b);
   return (float)sum * (a_is_more ? b : a) * (a_is_more ? a : b);
 }
 
