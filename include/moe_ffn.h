@@ -185,7 +185,8 @@ moe_status moe_w4_forward(const moe_shape* shape, int32_t group, const void* A,
  * of activations as codes and one scale. A vector x (a column of W, a row of X) has
  *   scale = max |x| / 127 rounded to fp32,  code = x / scale rounded to the nearest
  *   integer, ties to even (0 where the scale is 0, clamped to [-127, 127])
- * decided exactly. A vector that holds an infinity or NaN gets a scale of NaN and
+ * decided exactly, both of them (max |x| times the rounded 1 / 127 is another scale in 3 to 6%
+ * of the vectors). A vector that holds an infinity or NaN gets a scale of NaN and
  * codes 0: every product with it is NaN.
  *
  * moe_quantize_i8 gives the codes [E][K][N] and scales [E][N] of a bf16 or fp32
@@ -265,7 +266,8 @@ moe_status moe_i8_ffn_forward(const moe_ffn_shape* shape, const void* X, const v
  *
  * moe_few_i8_forward takes expert weights packed by moe_pack_i8_weights (E matrices; the
  * shared expert's with E = 1) and computes each expert as moe_i8_ffn_forward does; dtype
- * MOE_BF16 (A, W_router), H, D, D_shared multiples of 16.
+ * MOE_BF16 (A, W_router), H, D, D_shared multiples of 16. It is the one MoE call that takes
+ * such experts: above 128 tokens moe_forward does the layer, with weights in its own types.
  */
 size_t moe_few_workspace_bytes(const moe_shape* shape);    /* 0 if unsupported */
 moe_status moe_few_forward(const moe_shape* shape, const void* A, const void* W_router,

@@ -540,7 +540,9 @@ __global__ __launch_bounds__(kExpertThreads, 2) void few_up_kernel(FewArgs p) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) hv[q] = silu_f32(u[q]) * g[q];
       const int64_t to = (int64_t)row * D + d0 + c;
-      if constexpr (P == kBf16)  // rounded once, as the layer's h
+      // bf16: the down product's operand, rounded once as the layer's h is (2-norm error of O
+      // against 64 bits 0.0023 so, 0.0017 from O's own rounding alone)
+      if constexpr (P == kBf16)
         store_n(reinterpret_cast<bf16_t*>(p.h) + (shared ? (int64_t)p.F * p.D : 0) + to, hv);
       else
         store_shared(h, (uint32_t)to * 4, f32x4_t{hv[0], hv[1], hv[2], hv[3]});
