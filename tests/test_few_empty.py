@@ -1,11 +1,13 @@
 """A batch without tokens: every size query answers (in a process of its own, since a division
 by zero on the host would end this one), and the buffers' passes return nothing."""
+import os
 import subprocess
 import sys
 
 import pytest
 import torch
 
+import sparse_expert_ffn_amd as moe
 from sparse_expert_ffn_amd.layer import FewMoEBuffers, I8FFNBuffers, I8LinearBuffers, I8Weight
 
 QUERIES = [f"moe_few{i8}_workspace_bytes(m.make_shape(0, {H}, {D}, {E}, {k}, {Ds}))"
@@ -18,6 +20,8 @@ QUERIES += ["moe_few_workspace_bytes(m.make_shape(0, 64, 32, 4, 2, 32, dtype=m.M
 
 
 def test_sizes():
+    if not os.path.exists(moe.LIB_PATH):
+        moe.build()
     code = "import sparse_expert_ffn_amd as m\n"
     code += "\n".join(f"print(m.{q}, flush=True)" for q in QUERIES)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
